@@ -251,6 +251,115 @@ int dsa_sparse_mla_noalloc(const void* q, const void* kv, const int32_t* offsets
 int dsa_debug_stall_attention(int n_launches, uint64_t wait_limit_ns);
 
 /*
+ * ---------------------------------------------------------------- paged cache
+ *
+ * A latent cache in pages, for serving: the attention of new tokens over the
+ * whole of it (layers without an indexer, contexts below the top-k length),
+ * the attention weight that each slot collects, and the eviction of the slots
+ * that collect least.  The paper has no counterpart: the formulas are those
+ * of dsa_sparse_mla over every position.
+ *
+ *   kv_pages   [n_pages, page_size, 576] bf16, the pool of all sequences.
+ *              page_size is a multiple of 16, n_pages * page_size <= 2^31 - 4096.
+ *   page_table int32, row b at page_table + b * ld_table (ld_table >=
+ *              max_pages): slot s of sequence b is row
+ *              page_table[b, s / page_size] * page_size + s % page_size of the
+ *              pool.  Entries behind a sequence's last page are not read.
+ *   lens       int32 [B]: slots in use, the T newest tokens included (they sit
+ *              in the last T slots; query row t sees the slots s <= lens[b] -
+ *              T + t).  0 is an empty sequence (a padded batch) and fine
+ *              everywhere; a length outside [0, max_pages * page_size] is
+ *              reported as DSA_ERR_BAD_OFFSETS and treated as 0.
+ *   acc, pos   fp32 and int32, row b at acc + b * ld_slots: attention weight
+ *              collected by, and position of the token in, each slot.
+ *              16-byte aligned, ld_slots a multiple of 4 and >= every length.
+ * A page number outside [0, n_pages) is reported as DSA_ERR_BAD_INDEX; its
+ * slots count as masked.  Slots behind a sequence's length, and pages that no
+ * table names, are never written, and what they hold (NaN included) never
+ * reaches a result.  All sizes that change from step to step are read on the
+ * device, so one captured CUDA graph serves growing and shrinking sequences.
+ */
+
+/*
+ * Cache write of the T newest tokens of every sequence: slot lens[b] - T + t
+ * gets kv_new[b,t,:576], and, where the arrays are given (NULL: left out),
+ * acc = 0 and pos = end_pos[b] - T + t.  end_pos int32 [B]: tokens seen so far
+ * by the sequence, evicted ones included; needed with pos.  Two sequences may
+ * share pages for reading, not the pages written here.
+ * 0 < lens[b] < T is reported as DSA_ERR_BAD_OFFSETS and the sequence skipped.
+ */
+int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* page_table, int64_t ld_table,
+                     int max_pages, int B, int T, int page_size, int64_t n_pages, void* kv_pages, float* acc,
+                     int32_t* pos, const int32_t* end_pos, int64_t ld_slots, int32_t* dev_status, void* stream);
+
+/*
+ * Absorbed MLA of the T newest tokens over the whole paged cache (q, out, lse
+ * and scale as for dsa_sparse_mla):
+ *   l_s = scale * q[b,t,h,:576] . kv(b,s)[:576],  s <= lens[b] - T + t;  p = softmax_s(l)
+ *   out[b,t,h,:] = sum_s p_s * kv(b,s)[:512];  lse[b,t,h] = log sum_s exp(l_s)
+ * Rows that see no slot get out = 0, lse = -inf.
+ * workspace: dsa_paged_mla_workspace_size(B, T, H) bytes, for the current
+ * device; its contents need not survive between calls, and calls that may run
+ * at the same time need one each.
+ */
+size_t dsa_paged_mla_workspace_size(int B, int T, int H);
+int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,
+                  const int32_t* lens, int B, int T, int H, int page_size, int64_t n_pages, float scale, void* out,
+                  int out_dtype, float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Attention weight that every slot collects from these query rows:
+ *   acc_out[b,s] = decay * acc[b,s] + sum_{t,h : s <= lens[b]-T+t} exp(scale * q[b,t,h,:] . kv(b,s) - lse[b,t,h])
+ * for s < lens[b]; the other entries of acc_out are not touched.  lse comes
+ * from dsa_paged_mla with the same q, scale and cache; rows with lse = -inf
+ * add nothing.  acc may be NULL (zeros); acc_out may be acc.  A slot on a bad
+ * page gets decay * acc.  The sums' order is fixed: the same inputs always
+ * give the same bits.
+ */
+int dsa_paged_weights(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,
+                      const int32_t* lens, const float* lse, int B, int T, int H, int page_size, int64_t n_pages,
+                      float scale, float decay, const float* acc, float* acc_out, int64_t ld_slots,
+                      int32_t* dev_status, void* stream);
+
+/*
+ * Which slots stay when every sequence is cut to `budget` slots, and the row
+ * moves that close the gaps.  Of sequence b the n = min(budget, lens[b])
+ * first slots stay in this order: protected slots (pos >= end_pos[b] -
+ * recent; none when recent = 0) before the others, then larger acc, then the
+ * lower slot; NaN counts as less than everything, -0 as 0.  Survivors below n
+ * stay where they are; the i-th free slot below n takes the i-th survivor at
+ * or above n:
+ *   new_lens[b] = n,  n_moves[b] = number of moves (<= min(n, lens[b] - n)),
+ *   move_dst[b,i] (ascending), move_src[b,i] (ascending), -1 from n_moves[b]
+ *   up to ld_moves.
+ * Attention does not depend on the order of the slots, so nothing else has to
+ * move: the plan touches min(n, evicted) rows at most.  pos and end_pos may
+ * be NULL when recent = 0.  0 <= recent <= budget, budget >= 1.  A length
+ * outside [0, ld_slots], or more than ld_moves moves, is reported as
+ * DSA_ERR_BAD_OFFSETS; that sequence keeps its length and moves nothing.
+ * The outputs must not overlap the inputs, but new_lens may be lens.
+ * ld_slots above DSA_MAX_PLAN_SLOTS returns DSA_ERR_UNSUPPORTED.
+ */
+#define DSA_MAX_PLAN_SLOTS (6 << 20)
+int dsa_evict_plan(const float* acc, const int32_t* pos, const int32_t* lens, const int32_t* end_pos, int B,
+                   int64_t ld_slots, int budget, int recent, int32_t* new_lens, int32_t* n_moves, int32_t* move_dst,
+                   int32_t* move_src, int64_t ld_moves, int32_t* dev_status, void* stream);
+
+/*
+ * Carries a plan out: for i < n_moves[b] the cache row (and acc, pos where
+ * given, NULL: left out) of slot move_src[b,i] goes to slot move_dst[b,i].
+ * Moves run in parallel: no slot may be the destination of two moves or the
+ * source of one and the destination of another (a plan's never are).  Moves
+ * with a slot outside the page list (or ld_slots) or on a bad page are
+ * reported as DSA_ERR_BAD_INDEX and left out; an n_moves outside
+ * [0, ld_moves] is reported as DSA_ERR_BAD_OFFSETS and its sequence skipped.
+ */
+int dsa_paged_move(void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages, int page_size,
+                   int64_t n_pages, const int32_t* n_moves, const int32_t* move_dst, const int32_t* move_src,
+                   int64_t ld_moves, int B, float* acc, int32_t* pos, int64_t ld_slots, int32_t* dev_status,
+                   void* stream);
+
+/*
  * Where, inside a decode-step workspace, the step leaves its intermediates
  * (byte offsets; the scores pitch is returned in *ld_scores).  For tests and
  * tools that want to look at stage outputs; the layout may change between

@@ -24,7 +24,9 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_indexer_scores", "dsa_topk",
            "dsa_sparse_mla_workspace_size", "dsa_sparse_mla", "dsa_decode_step_workspace_size",
            "dsa_decode_step", "dsa_decode_step_workspace_layout", "dsa_sparse_mla_noalloc",
            "dsa_decode_step_launches", "dsa_cache_append", "dsa_quantize_queries", "dsa_indexer_prestage",
-           "dsa_copy_host_to_device", "dsa_copy_device_to_host", "dsa_debug_stall_attention")
+           "dsa_copy_host_to_device", "dsa_copy_device_to_host", "dsa_debug_stall_attention",
+           "dsa_paged_append", "dsa_paged_mla_workspace_size", "dsa_paged_mla", "dsa_paged_weights",
+           "dsa_evict_plan", "dsa_paged_move")
 
 
 class DSAError(RuntimeError):
@@ -56,6 +58,12 @@ def _load():
         "dsa_copy_host_to_device": ([P, P, SZ, P], I),
         "dsa_copy_device_to_host": ([P, P, SZ, P], I),
         "dsa_debug_stall_attention": ([I, ctypes.c_uint64], I),
+        "dsa_paged_append": ([P, P, P, I64, I, I, I, I, I64, P, P, P, P, I64, P, P], I),
+        "dsa_paged_mla_workspace_size": ([I, I, I], SZ),
+        "dsa_paged_mla": ([P, P, P, I64, I, P, I, I, I, I, I64, F, P, I, P, P, SZ, P, P], I),
+        "dsa_paged_weights": ([P, P, P, I64, I, P, P, I, I, I, I, I64, F, F, P, P, I64, P, P], I),
+        "dsa_evict_plan": ([P, P, P, P, I, I64, I, I, P, P, P, P, I64, P, P], I),
+        "dsa_paged_move": ([P, P, I64, I, I, I64, P, P, P, I64, I, P, P, I64, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -218,3 +226,162 @@ def decode_step(q_idx, w, k_idx, k_scale, q, kv, offsets, B, max_end_pos, kv_row
                                _p(offsets), B, max_end_pos, kv_rows, k, H, float(scale), _p(out), out_code,
                                _p(lse), _p(workspace), ws_bytes, _p(status), _stream(stream)),
            "dsa_decode_step")
+
+
+# ---- paged cache.  Sizes are taken from the tensors and checked against each
+# other here: the library sees pointers only.
+
+def _arg(t, dtype, shape, what, dev, rows=False):
+    """Pointer of a CUDA tensor of this type and shape on `dev`; None gives NULL.
+    rows: a 2-D tensor whose rows may lie further apart than they are long."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape:
+        raise DSAError(1, f"{what} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if t.device != dev:
+        raise DSAError(1, f"{what} is on {t.device}, not on {dev}")
+    if rows:
+        if t.numel() and (t.stride(1) != 1 or (t.stride(0) < shape[1] and shape[0] > 1)):
+            raise DSAError(1, f"the rows of {what} are not contiguous")
+    elif not t.is_contiguous():
+        raise DSAError(1, f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+def _row_pitch(t):
+    """Elements from one row of a 2-D tensor to the next."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _run_on(dev, stream, fn, what, *args):
+    """fn(*args, stream) on `dev`, whatever device is current."""
+    if stream is not None and stream.device != dev:
+        raise DSAError(1, f"{what}: the stream is on {stream.device}, the tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    _check(rc, what)
+
+
+def _pages(kv_pages, page_table, what):
+    """(device, B, page_size, n_pages) of a paged cache, checked."""
+    if kv_pages.dim() != 3 or kv_pages.shape[2] != 576 or kv_pages.dtype is not torch.bfloat16:
+        raise DSAError(1, f"{what}: kv_pages must be bfloat16 [n_pages, page_size, 576]")
+    if not kv_pages.is_cuda:
+        raise DSAError(1, f"{what}: kv_pages is not on a CUDA device")
+    if page_table.dim() != 2:
+        raise DSAError(1, f"{what}: page_table must be [B, max_pages]")
+    return kv_pages.device, page_table.shape[0], kv_pages.shape[1], kv_pages.shape[0]
+
+
+def _slots(acc, pos, B, dev):
+    """(acc, pos, ld_slots): pointers and row length of the per-slot arrays [B, slots]."""
+    one = acc if acc is not None else pos
+    if one is None:
+        return None, None, 0
+    if one.dim() != 2:
+        raise DSAError(1, "acc and pos must be [B, slots]")
+    shape = (B, one.shape[1])
+    return _arg(acc, torch.float32, shape, "acc", dev), _arg(pos, torch.int32, shape, "pos", dev), shape[1]
+
+
+def _out_code(out, shape, dev):
+    """DSA_BF16 or DSA_F32 of an output tensor, and its pointer."""
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise DSAError(1, f"out must be bfloat16 or float32, not {out.dtype}")
+    return (DSA_BF16 if out.dtype is torch.bfloat16 else DSA_F32), _arg(out, out.dtype, shape, "out", dev)
+
+
+def paged_append(kv_new, kv_pages, page_table, lens, acc=None, pos=None, end_pos=None, status=None, stream=None):
+    """dsa_paged_append: the newest T tokens' rows kv_new [B,T,576] into each
+    sequence's last T slots, acc = 0 and pos = end_pos - T + t beside them."""
+    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_append")
+    if kv_new.dim() != 3:
+        raise DSAError(1, "paged_append: kv_new must be [B, T, 576]")
+    T = kv_new.shape[1]
+    a, p, ld = _slots(acc, pos, B, dev)
+    _run_on(dev, stream, lib.dsa_paged_append, "dsa_paged_append",
+            _arg(kv_new, torch.bfloat16, (B, T, 576), "kv_new", dev), _arg(lens, torch.int32, (B,), "lens", dev),
+            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
+            page_table.shape[1], B, T, P, n_pages, _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
+            a, p, _arg(end_pos, torch.int32, (B,), "end_pos", dev), ld, _arg(status, torch.int32, (1,), "status", dev))
+
+
+def paged_mla_workspace_size(B, T, H) -> int:
+    """Workspace bytes of paged_mla on the current device."""
+    return int(lib.dsa_paged_mla_workspace_size(B, T, H))
+
+
+def paged_mla(q, kv_pages, page_table, lens, scale, out, lse=None, workspace=None, status=None, stream=None):
+    """dsa_paged_mla: attention of q [B,T,H,576] over the whole paged cache
+    into out [B,T,H,512] (bf16 or fp32 by out's dtype) and lse [B,T,H]."""
+    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_mla")
+    if q.dim() != 4:
+        raise DSAError(1, "paged_mla: q must be [B, T, H, 576]")
+    T, H = q.shape[1], q.shape[2]
+    code, o = _out_code(out, (B, T, H, 512), dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws = None if workspace is None else _arg(workspace, workspace.dtype, tuple(workspace.shape), "workspace", dev)
+    _run_on(dev, stream, lib.dsa_paged_mla, "dsa_paged_mla", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev),
+            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
+            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
+            page_table.shape[1], _arg(lens, torch.int32, (B,), "lens", dev), B, T, H, P, n_pages, float(scale), o, code,
+            _arg(lse, torch.float32, (B, T, H), "lse", dev), ws, ws_bytes, _arg(status, torch.int32, (1,), "status", dev))
+
+
+def paged_weights(q, kv_pages, page_table, lens, lse, scale, acc, acc_out=None, decay=1.0, status=None, stream=None):
+    """dsa_paged_weights: acc_out [B,slots] = decay * acc + the attention
+    weight every slot gets from q [B,T,H,576].  acc_out: acc itself unless
+    given; acc=None counts as zeros."""
+    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_weights")
+    if q.dim() != 4:
+        raise DSAError(1, "paged_weights: q must be [B, T, H, 576]")
+    T, H = q.shape[1], q.shape[2]
+    if acc_out is None:
+        acc_out = acc
+    if acc_out is None:
+        raise DSAError(1, "paged_weights: acc or acc_out is needed")
+    o, _, ld = _slots(acc_out, None, B, dev)
+    a = o if acc is acc_out else _arg(acc, torch.float32, (B, ld), "acc", dev)
+    _run_on(dev, stream, lib.dsa_paged_weights, "dsa_paged_weights",
+            _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev),
+            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
+            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
+            page_table.shape[1], _arg(lens, torch.int32, (B,), "lens", dev),
+            _arg(lse, torch.float32, (B, T, H), "lse", dev), B, T, H, P, n_pages, float(scale), float(decay), a, o, ld,
+            _arg(status, torch.int32, (1,), "status", dev))
+
+
+def evict_plan(acc, pos, lens, end_pos, budget, recent, new_lens, n_moves, move_dst, move_src, status=None, stream=None):
+    """dsa_evict_plan: new lengths and the move list that cut every sequence
+    to `budget` slots (pos and end_pos may be None when recent is 0)."""
+    if acc.dim() != 2 or move_dst.dim() != 2:
+        raise DSAError(1, "evict_plan: acc must be [B, slots], move_dst and move_src [B, moves]")
+    if not acc.is_cuda:
+        raise DSAError(1, "evict_plan: acc is not on a CUDA device")
+    dev, B, moves = acc.device, acc.shape[0], tuple(move_dst.shape)
+    if moves[0] != B:
+        raise DSAError(1, "evict_plan: move_dst and move_src need a row per sequence")
+    a, p, ld = _slots(acc, pos, B, dev)
+    _run_on(dev, stream, lib.dsa_evict_plan, "dsa_evict_plan", a, p, _arg(lens, torch.int32, (B,), "lens", dev),
+            _arg(end_pos, torch.int32, (B,), "end_pos", dev), B, ld, int(budget), int(recent),
+            _arg(new_lens, torch.int32, (B,), "new_lens", dev), _arg(n_moves, torch.int32, (B,), "n_moves", dev),
+            _arg(move_dst, torch.int32, moves, "move_dst", dev), _arg(move_src, torch.int32, moves, "move_src", dev),
+            moves[1], _arg(status, torch.int32, (1,), "status", dev))
+
+
+def paged_move(kv_pages, page_table, n_moves, move_dst, move_src, acc=None, pos=None, status=None, stream=None):
+    """dsa_paged_move: carries an eviction plan out on the cache, acc and pos."""
+    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_move")
+    if move_dst.dim() != 2 or move_dst.shape[0] != B:
+        raise DSAError(1, "paged_move: move_dst and move_src must be [B, moves]")
+    moves = tuple(move_dst.shape)
+    a, p, ld = _slots(acc, pos, B, dev)
+    _run_on(dev, stream, lib.dsa_paged_move, "dsa_paged_move",
+            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
+            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
+            page_table.shape[1], P, n_pages, _arg(n_moves, torch.int32, (B,), "n_moves", dev),
+            _arg(move_dst, torch.int32, moves, "move_dst", dev), _arg(move_src, torch.int32, moves, "move_src", dev),
+            moves[1], B, a, p, ld, _arg(status, torch.int32, (1,), "status", dev))

@@ -1,0 +1,318 @@
+// evict_plan.cu -- which slots of a paged cache survive a cut to `budget`
+// slots, and the row moves that close the gaps.
+//
+// Per sequence of L > n = budget slots: every slot gets a 32-bit key (order-
+// preserving in acc; all ones where the slot is protected, 0 for NaN), three
+// digit passes (11, 11, 10 bits) over the keys find the n-th largest key tau
+// and how many keys equal to tau stay (the lowest slots), and two prefix
+// counts over the resulting bitmap rank the free slots below n and the
+// survivors from n on: the i-th of one takes the i-th of the other.
+//
+// One thread-block cluster per sequence; CTA r owns the contiguous slots
+// [r * S, (r + 1) * S).  The slots' acc and pos are read from memory once
+// (HBM bounds a large plan at 8 bytes per slot); the keys stay in shared
+// memory as far as it goes (about 46000 per CTA) and are made again from
+// memory above that.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCS = 8;
+constexpr int kSmemMax = 227 * 1024;
+
+struct PlanSmem {
+  uint32_t hist[3][kBins];  // one per pass: no CTA clears what another still reads
+  uint32_t tot[kBins];      // cluster-wide counts of the current pass
+  uint32_t warp_tot[kWarps];
+  uint32_t cnt[2];          // this CTA's free slots below n, survivors from n on
+  uint32_t base[2];         // those of the CTAs before it
+  uint32_t total;           // moves of the sequence
+  uint32_t digit, remaining, eq_before;
+};
+
+static_assert((int64_t)sizeof(PlanSmem) + 8 * (DSA_MAX_PLAN_SLOTS / kMaxCS / 32 + 4) <= kSmemMax, "shared memory");
+
+struct PlanArgs {
+  const float* acc;
+  const int32_t* pos;
+  const int32_t* lens;
+  const int32_t* end_pos;
+  int64_t ld;
+  int budget, recent;
+  int32_t* new_lens;
+  int32_t* n_moves;
+  int32_t* dst;
+  int32_t* src;
+  int64_t ld_moves;
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t slot_key(float a, bool kept_always) {
+  if (kept_always) return 0xffffffffu;
+  return a != a ? 0u : float_order_key(a);  // -inf maps above 0
+}
+
+// Exclusive scan over the block of one value per thread; *total is the sum.
+__device__ __forceinline__ uint32_t scan_excl(uint32_t v, PlanSmem& sm, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();  // warp_tot may still be read from the scan before
+  if (lane == 31) sm.warp_tot[warp] = inc;
+  __syncthreads();
+  const uint32_t w = sm.warp_tot[lane];
+  uint32_t winc = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, winc, o);
+    if (lane >= o) winc += u;
+  }
+  *total = __shfl_sync(0xffffffffu, winc, 31);
+  return inc - v + __shfl_sync(0xffffffffu, winc - w, warp);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs a, int key_cap) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  PlanSmem& sm = *reinterpret_cast<PlanSmem*>(smem_raw);
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(smem_raw + sizeof(PlanSmem));  // key_cap, then the bitmap
+  uint32_t* const bitmap = keys + key_cap;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / CS;
+
+  grid_dependency_wait();  // acc and lens come from the previous kernel
+  allow_dependents_launch();
+  const int32_t L = a.lens[b];
+  const bool bad = L < 0 || (int64_t)L > a.ld;
+  const int32_t n = min(L, a.budget);
+  int32_t* const dst = a.dst + (int64_t)b * a.ld_moves;
+  int32_t* const src = a.src + (int64_t)b * a.ld_moves;
+  auto pad_lists = [&](int64_t from) {
+    for (int64_t i = from + (int64_t)rank * kThreads + threadIdx.x; i < a.ld_moves; i += (int64_t)CS * kThreads) {
+      dst[i] = -1;
+      src[i] = -1;
+    }
+  };
+  if (bad || L <= a.budget) {  // nothing to evict (the same verdict in every CTA)
+    if (rank == 0 && threadIdx.x == 0) {
+      if (bad) report(a.status, DSA_ERR_BAD_OFFSETS);
+      a.new_lens[b] = L;
+      a.n_moves[b] = 0;
+    }
+    pad_lists(0);
+    return;
+  }
+  const int S = ((L + CS - 1) / CS + 127) / 128 * 128;
+  const int s_lo = min(rank * S, L), m = min(s_lo + S, L) - s_lo;  // this CTA's slots
+  const float* const acc = a.acc + (int64_t)b * a.ld + s_lo;
+  const int32_t* const pos = a.recent > 0 ? a.pos + (int64_t)b * a.ld + s_lo : nullptr;
+  const int64_t protect_from = a.recent > 0 ? (int64_t)a.end_pos[b] - a.recent : 0;
+  auto make_key = [&](int i) { return slot_key(acc[i], pos && pos[i] >= protect_from); };
+  auto key_of = [&](int i) { return i < key_cap ? keys[i] : make_key(i); };
+
+  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+  __syncthreads();
+  // ---- keys, and the histogram of their top 11 bits
+  auto count = [&](uint32_t* hist, uint32_t bin, bool on) {
+    // a warp of equal keys (fresh slots, say) adds once
+    const uint32_t mask = __ballot_sync(0xffffffffu, on);
+    if (mask == 0) return;
+    const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(mask) - 1);
+    if (__all_sync(0xffffffffu, !on || bin == first)) {
+      if (lane == 0) atomicAdd(&hist[first], (uint32_t)__popc(mask));
+    } else if (on) {
+      atomicAdd(&hist[bin], 1u);
+    }
+  };
+  for (int i0 = 0; i0 < m; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const uint32_t key = i < m ? make_key(i) : 0u;
+    if (i < m && i < key_cap) keys[i] = key;
+    count(sm.hist[0], key >> 21, i < m);
+  }
+  // ---- three digit passes: tau, and how many keys equal to it stay
+  uint32_t prefix = 0, remaining = (uint32_t)n;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    if (pass > 0) {
+      const int pshift = pass == 1 ? 21 : 10;
+      for (int i0 = 0; i0 < m; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const uint32_t key = i < m ? key_of(i) : 0u;
+        count(sm.hist[pass], (key >> shift) & (uint32_t)(bins - 1), i < m && (key >> pshift) == (prefix >> pshift));
+      }
+    }
+    cluster.sync();
+    for (int i = threadIdx.x; i < bins; i += kThreads) {
+      uint32_t v = 0;
+      for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(&sm.hist[pass][0], q)[i];
+      sm.tot[i] = v;
+    }
+    __syncthreads();
+    // the bin, from the top, that holds the remaining-th largest key: thread
+    // t takes the bins bins-1-2t and bins-2-2t
+    const int hi = bins - 1 - 2 * (int)threadIdx.x;
+    const uint32_t c0 = hi > 0 ? sm.tot[hi] : 0u, c1 = hi > 0 ? sm.tot[hi - 1] : 0u;
+    uint32_t all;
+    const uint32_t above = scan_excl(c0 + c1, sm, &all);
+    if (above < remaining && remaining <= above + c0 + c1) {
+      const bool second = remaining > above + c0;
+      sm.digit = (uint32_t)(second ? hi - 1 : hi);
+      sm.remaining = remaining - above - (second ? c0 : 0u);
+    }
+    __syncthreads();
+    prefix |= sm.digit << shift;
+    remaining = sm.remaining;
+    __syncthreads();
+  }
+  const uint32_t tau = prefix, need_eq = remaining;
+  if (warp == 0) {  // keys equal to tau in the CTAs before this one
+    uint32_t v = lane < rank ? cluster.map_shared_rank(&sm.hist[2][0], lane)[tau & 1023u] : 0u;
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (lane == 0) sm.eq_before = v;
+  }
+  __syncthreads();
+  // ---- which slots stay: a bitmap, one word per 32 slots; thread t owns a
+  // contiguous run of words
+  const int words = (m + 31) / 32;
+  const int wpt = (words + kThreads - 1) / kThreads;
+  for (int w = warp; w < words; w += kWarps) {
+    const int i = 32 * w + lane;
+    const uint32_t key = i < m ? key_of(i) : 0u;
+    const uint32_t up = __ballot_sync(0xffffffffu, i < m && key > tau);
+    const uint32_t eq = __ballot_sync(0xffffffffu, i < m && key == tau);
+    if (lane == 0) {
+      bitmap[2 * w] = up;
+      bitmap[2 * w + 1] = eq;
+    }
+  }
+  __syncthreads();
+  const int w_lo = min((int)threadIdx.x * wpt, words), w_hi = min(w_lo + wpt, words);
+  uint32_t eqs = 0, unused;
+  for (int w = w_lo; w < w_hi; ++w) eqs += __popc(bitmap[2 * w + 1]);
+  uint32_t eq_rank = sm.eq_before + scan_excl(eqs, sm, &unused);
+  // slots of word w below n
+  auto below = [&](int w) -> uint32_t {
+    const int k = n - (s_lo + 32 * w);
+    return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+  };
+  auto held = [&](int w) -> uint32_t { return m - 32 * w >= 32 ? 0xffffffffu : (1u << (m - 32 * w)) - 1u; };
+  uint32_t free_n = 0, surv_n = 0;
+  for (int w = w_lo; w < w_hi; ++w) {
+    uint32_t keep = bitmap[2 * w], eq = bitmap[2 * w + 1];
+    while (eq && eq_rank < need_eq) {
+      const uint32_t low = eq & (0u - eq);
+      keep |= low;
+      eq ^= low;
+      ++eq_rank;
+    }
+    bitmap[2 * w] = keep;
+    free_n += __popc(~keep & below(w) & held(w));
+    surv_n += __popc(keep & ~below(w));
+  }
+  uint32_t free_all, surv_all;
+  uint32_t fr = scan_excl(free_n, sm, &free_all);
+  uint32_t sr = scan_excl(surv_n, sm, &surv_all);
+  if (threadIdx.x == 0) {
+    sm.cnt[0] = free_all;
+    sm.cnt[1] = surv_all;
+  }
+  cluster.sync();
+  if (warp == 0) {
+    const uint32_t f = lane < CS ? cluster.map_shared_rank(&sm.cnt[0], lane)[0] : 0u;
+    const uint32_t s = lane < rank ? cluster.map_shared_rank(&sm.cnt[0], lane)[1] : 0u;
+    const uint32_t total = __reduce_add_sync(0xffffffffu, f);
+    const uint32_t f_before = __reduce_add_sync(0xffffffffu, lane < rank ? f : 0u);
+    const uint32_t s_before = __reduce_add_sync(0xffffffffu, s);
+    if (lane == 0) {
+      sm.total = total;
+      sm.base[0] = f_before;
+      sm.base[1] = s_before;
+    }
+  }
+  cluster.sync();  // also: no CTA leaves while another reads its counts
+  const uint32_t moves = sm.total;
+  if ((int64_t)moves > a.ld_moves) {
+    if (rank == 0 && threadIdx.x == 0) {
+      report(a.status, DSA_ERR_BAD_OFFSETS);
+      a.new_lens[b] = L;
+      a.n_moves[b] = 0;
+    }
+    pad_lists(0);
+    return;
+  }
+  fr += sm.base[0];
+  sr += sm.base[1];
+  for (int w = w_lo; w < w_hi; ++w) {
+    uint32_t f = ~bitmap[2 * w] & below(w) & held(w), s = bitmap[2 * w] & ~below(w);
+    for (; f; f &= f - 1) dst[fr++] = s_lo + 32 * w + __ffs((int)f) - 1;
+    for (; s; s &= s - 1) src[sr++] = s_lo + 32 * w + __ffs((int)s) - 1;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    a.new_lens[b] = n;
+    a.n_moves[b] = (int32_t)moves;
+  }
+  pad_lists(moves);
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int dsa_evict_plan(const float* acc, const int32_t* pos, const int32_t* lens, const int32_t* end_pos, int B,
+                              int64_t ld_slots, int budget, int recent, int32_t* new_lens, int32_t* n_moves,
+                              int32_t* move_dst, int32_t* move_src, int64_t ld_moves, int32_t* dev_status,
+                              void* stream) {
+  if (B <= 0 || !acc || !lens || !new_lens || !n_moves || !move_dst || !move_src || ld_moves < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (B > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if (budget < 1 || recent < 0 || recent > budget) return DSA_ERR_INVALID_ARG;
+  if (recent > 0 && (!pos || !end_pos)) return DSA_ERR_INVALID_ARG;
+  if (int rc = check_slots(acc, pos, ld_slots)) return rc;
+  if (ld_slots > DSA_MAX_PLAN_SLOTS) return DSA_ERR_UNSUPPORTED;
+  // CTAs per sequence: one per 8192 slots, up to eight (a portable cluster)
+  int cs = 1;
+  while (cs < kMaxCS && ld_slots > (int64_t)8192 * cs) cs *= 2;
+  const int64_t slice = ((ld_slots + cs - 1) / cs + 127) / 128 * 128;
+  const int64_t fixed = (int64_t)sizeof(PlanSmem) + 8 * ((slice + 31) / 32);
+  const int key_cap = (int)std::min<int64_t>(slice, (kSmemMax - fixed) / 4);
+  const int64_t smem = fixed + 4 * (int64_t)key_cap;
+  static PerDeviceOnce attr;
+  if (attr.run([] {
+        return cudaFuncSetAttribute(evict_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+      }) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const PlanArgs a{acc, pos, lens, end_pos, ld_slots, budget, recent, new_lens, n_moves, move_dst, move_src, ld_moves, dev_status};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)B * (unsigned)cs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cs;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_plan_kernel, a, key_cap) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}

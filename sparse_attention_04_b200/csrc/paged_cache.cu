@@ -1,0 +1,137 @@
+// paged_cache.cu -- row traffic of the paged latent cache: the write of the
+// newest tokens and the row moves of an eviction.
+//
+// Both only move bytes: a token is one 1152-byte row (576 bf16) read and
+// written, plus its acc and pos entries.  HBM bounds them for prompts and
+// large evictions, launch latency for single steps.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kRowPieces = kDQK / 8;  // 16-byte pieces per row: 72
+
+// One warp copies one row: lanes take the pieces l, l + 32, l + 64.
+__device__ __forceinline__ void copy_row(uint4* __restrict__ dst, const uint4* __restrict__ src, int lane) {
+  const uint4 a = src[lane], b = src[lane + 32];
+  uint4 c;
+  if (lane < kRowPieces - 64) c = src[lane + 64];
+  dst[lane] = a;
+  dst[lane + 32] = b;
+  if (lane < kRowPieces - 64) dst[lane + 64] = c;
+}
+
+// One warp per new token (b, t).
+__global__ void __launch_bounds__(256)
+    paged_append_kernel(const __nv_bfloat16* __restrict__ kv_new, const int32_t* __restrict__ lens, PagePool pool, int B,
+                        int T, __nv_bfloat16* __restrict__ kv, float* __restrict__ acc, int32_t* __restrict__ pos,
+                        const int32_t* __restrict__ end_pos, int64_t ld_slots, int32_t* status) {
+  grid_dependency_wait();  // the new rows may come from the previous kernel
+  allow_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t tok = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (tok >= (int64_t)B * T) return;
+  const int b = (int)(tok / T), t = (int)(tok - (int64_t)b * T);
+  bool bad;
+  int64_t cap = pool_capacity(pool);
+  if (acc || pos) cap = min(cap, ld_slots);
+  const int32_t len = checked_len(lens[b], cap, bad);
+  if (bad || (len > 0 && len < T)) {
+    if (lane == 0) report(status, DSA_ERR_BAD_OFFSETS);
+    return;
+  }
+  if (len == 0) return;
+  const int32_t slot = len - T + t;
+  const int64_t row = pool_row(pool, b, slot);
+  if (row < 0) {
+    if (lane == 0) report(status, DSA_ERR_BAD_INDEX);
+  } else {
+    copy_row(reinterpret_cast<uint4*>(kv + row * kDQK), reinterpret_cast<const uint4*>(kv_new + tok * kDQK), lane);
+  }
+  if (lane == 0) {
+    if (acc) acc[(int64_t)b * ld_slots + slot] = 0.f;
+    if (pos) pos[(int64_t)b * ld_slots + slot] = end_pos[b] - T + t;
+  }
+}
+
+// One warp per move, the grid's y walks the sequences.
+__global__ void __launch_bounds__(256)
+    paged_move_kernel(__nv_bfloat16* kv, PagePool pool, const int32_t* __restrict__ n_moves,
+                      const int32_t* __restrict__ move_dst, const int32_t* __restrict__ move_src, int64_t ld_moves, int B,
+                      float* acc, int32_t* pos, int64_t ld_slots, int32_t* status) {
+  grid_dependency_wait();  // the plan may come from the previous kernel
+  allow_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  int64_t cap = pool_capacity(pool);
+  if (acc || pos) cap = min(cap, ld_slots);
+  for (int b = blockIdx.y; b < B; b += gridDim.y) {
+    const int32_t n = n_moves[b];
+    if (n < 0 || n > ld_moves) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) report(status, DSA_ERR_BAD_OFFSETS);
+      continue;
+    }
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
+      const int32_t d = move_dst[(int64_t)b * ld_moves + i], s = move_src[(int64_t)b * ld_moves + i];
+      const bool in = d >= 0 && s >= 0 && d < cap && s < cap;
+      const int64_t rd = in ? pool_row(pool, b, d) : -1, rs = in ? pool_row(pool, b, s) : -1;
+      if (rd < 0 || rs < 0) {
+        if (lane == 0) report(status, DSA_ERR_BAD_INDEX);
+        continue;
+      }
+      copy_row(reinterpret_cast<uint4*>(kv + rd * kDQK), reinterpret_cast<const uint4*>(kv + rs * kDQK), lane);
+      if (lane == 0) {
+        const int64_t o = (int64_t)b * ld_slots;
+        if (acc) acc[o + d] = acc[o + s];
+        if (pos) pos[o + d] = pos[o + s];
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* page_table, int64_t ld_table,
+                     int max_pages, int B, int T, int page_size, int64_t n_pages, void* kv_pages, float* acc,
+                     int32_t* pos, const int32_t* end_pos, int64_t ld_slots, int32_t* dev_status, void* stream) {
+  if (B <= 0 || T <= 0 || !kv_new || !lens || !is_aligned16(kv_new)) return DSA_ERR_INVALID_ARG;
+  if ((int64_t)B * T > (int64_t)1 << 24) return DSA_ERR_UNSUPPORTED;
+  if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
+  if (int rc = check_slots(acc, pos, ld_slots)) return rc;
+  if (pos && !end_pos) return DSA_ERR_INVALID_ARG;
+  const PagePool pool{page_table, ld_table, n_pages, max_pages, page_size};
+  const int64_t toks = (int64_t)B * T;
+  const cudaError_t e =
+      launch_pdl(paged_append_kernel, dim3((unsigned)((toks + 7) / 8)), dim3(256), 0,
+                 reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const __nv_bfloat16*>(kv_new), lens, pool, B, T,
+                 reinterpret_cast<__nv_bfloat16*>(kv_pages), acc, pos, end_pos, ld_slots, dev_status);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int dsa_paged_move(void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages, int page_size,
+                   int64_t n_pages, const int32_t* n_moves, const int32_t* move_dst, const int32_t* move_src,
+                   int64_t ld_moves, int B, float* acc, int32_t* pos, int64_t ld_slots, int32_t* dev_status,
+                   void* stream) {
+  if (B <= 0 || !n_moves || !move_dst || !move_src || ld_moves < 1) return DSA_ERR_INVALID_ARG;
+  if (B > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
+  if (int rc = check_slots(acc, pos, ld_slots)) return rc;
+  const PagePool pool{page_table, ld_table, n_pages, max_pages, page_size};
+  // About eight CTAs of eight warps per SM over all sequences (the lists'
+  // lengths are known on the device only), fewer where the lists are short.
+  const int64_t y = std::min<int64_t>(B, 32768);
+  const int64_t x = std::min<int64_t>((ld_moves + 7) / 8, std::max<int64_t>(1, (8 * (int64_t)device_info().sm_count + y - 1) / y));
+  const cudaError_t e =
+      launch_pdl(paged_move_kernel, dim3((unsigned)x, (unsigned)y), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream),
+                 reinterpret_cast<__nv_bfloat16*>(kv_pages), pool, n_moves, move_dst, move_src, ld_moves, B, acc, pos,
+                 ld_slots, dev_status);
+  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // extern "C"
