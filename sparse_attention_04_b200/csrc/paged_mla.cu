@@ -3,83 +3,915 @@
 // For query row (b, t) and head h, over the slots s <= lens[b] - T + t:
 //   l_s = scale * q . kv_s[:576];  out = softmax(l) . kv[:, :512];  lse = log sum exp(l)
 //
-// Plain form: one CTA per (row, 8 heads), one warp per head; 32 slots at a
-// time are staged in shared memory, each lane scores one of them, and the
-// running maximum and sum of the softmax are kept in fp32.
+// With 128 heads a slot costs 2 * 128 * (576 + 512) flops and 1152 bytes: 242
+// flops per byte, the ratio of this card's measured rates, so the kernel has
+// to keep the tensor cores and the memory busy at the same time.  With fewer
+// heads the memory bounds it.
+//
+// Split.  The rows' 128-slot chunks form one list; every cluster of two CTAs
+// takes an equal, contiguous part of it, whatever the sequences' lengths
+// (they are read on the device).  A row that lies in one cluster's part is
+// finished there; a row cut by part boundaries leaves one fp32 partial per
+// cluster, joined by paged_mla_combine_kernel.  At most two partials per
+// cluster exist (the row that begins before its part, the row that goes on
+// behind it).
+//
+// Two CTAs.  A 128-head tile's output fills an SM's tensor memory (128 lanes x
+// 512 fp32 columns), so the pair divides the work by role:
+//   CTA 0 (QK side): query blocks 0-7 (64 columns each) in TMEM, block 8 in
+//     shared memory; a chunk's rows arrive by TMA as nine 128 x 64 blocks in a
+//     ring of eight; S = Q.K^T (N = 128) goes to one of two TMEM buffers.
+//     Eight softmax warps, thread = (head, half of the chunk's slots); the
+//     halves' maxima meet in shared memory, P is rounded to bf16 (the tensor
+//     core's operand; its sum l is kept unrounded in fp32) and sent to CTA 1
+//     by the copy engine, 64 slots at a time, with the rescale factor.
+//   CTA 1 (PV side): O in TMEM.  The rows' first 512 columns arrive by TMA as
+//     64-slot x 256-column tiles in a ring of five (they come out of L2, where
+//     CTA 0's loads have put them); O += P.V in two N = 256 halves per 64
+//     slots.  O is rescaled only when a row's running maximum rose by more
+//     than 2^8 (P then stays below 2^8 and keeps its relative precision).
+// TMA boxes are the largest of 64, 32, 16 rows that divides the page size, so
+// that no box crosses a page.  Boxes behind the row's end, or on a bad page,
+// are asked for outside the tensor and arrive as zeros; slots behind the end
+// inside the last box are zeroed in CTA 1 before the product (their P is 0,
+// but they may hold NaN) and masked in CTA 0.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "paged.cuh"
+#include "tmap.h"
 
 namespace dsa {
 namespace {
 
-constexpr int kHeads = 8, kTile = 32, kRowPad = kDQK + 8;
+constexpr int kChunk = 128;              // slots per chunk: the QK product's N
+constexpr int kSub = 64;                 // slots per message to CTA 1
+constexpr int kKB = kDQK / 64;           // 64-column blocks of a row: 9
+constexpr int kKBlockBytes = kChunk * 128;
+constexpr int kRowUnits = 2;             // what a row costs besides its chunks, in chunks
 
-__global__ void __launch_bounds__(256)
-    paged_mla_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kv, PagePool pool,
-                     const int32_t* __restrict__ lens, int T, int H, float scale_log2, void* out, int out_bf16, float* lse,
-                     int32_t* status) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem_raw);      // [32][584]
-  float* sq = reinterpret_cast<float*>(smem_raw + kTile * kRowPad * 2);  // [8][576]
-  __shared__ int s_ok[kTile];
+constexpr int kThreads = 384;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10;
+constexpr int kSoftmaxThreads = 256;
+
+constexpr int kPBytes = 128 * kSub * 2;             // P: 128 heads x 64 slots, bf16
+constexpr uint32_t kMsgBytes = kPBytes + 3 * 512;   // then alpha, l, m per head
+// ---- CTA 0 shared memory
+constexpr int kQ8Off = 0;
+constexpr int kKSlots = 8;
+constexpr int kKRingOff = kKBlockBytes;
+constexpr int kStages = 4;
+constexpr int kStageOff = kKRingOff + kKSlots * kKBlockBytes;     // 147456
+constexpr int kMaxOff = kStageOff + kStages * (int)kMsgBytes;     // 219136: maxima [2][2][128]
+constexpr int kMaskOff = kMaxOff + 2 * 2 * 128 * 4;               // validity words [4][4]
+constexpr int kQkEnd = kMaskOff + 4 * 16;
+// ---- CTA 1 shared memory
+constexpr int kVSlotBytes = kSub * 512;             // 64 slots x 256 columns
+constexpr int kVBlockBytes = kSub * 128;            // 64 slots x 64 columns
+constexpr int kVSlots = 5;
+constexpr int kPBufs = 3;
+constexpr int kPOff = kVSlots * kVSlotBytes;                      // 163840
+constexpr int kOutOff = kPOff + kPBufs * (int)kMsgBytes;          // 217600: epilogue staging, 2 KB per warp
+constexpr int kPvEnd = kOutOff + 4 * 2048;
+// ---- both
+constexpr int kBarOff = (kQkEnd > kPvEnd ? kQkEnd : kPvEnd);
+enum Bar : int {
+  kQFull = 0,
+  kKFull = 1,                       // [8] CTA 0
+  kKEmpty = kKFull + kKSlots,       // [8] CTA 0
+  kSFull = kKEmpty + kKSlots,       // [2] CTA 0
+  kSEmpty = kSFull + 2,             // [2] CTA 0
+  kMaskFull = kSEmpty + 2,          // [4] CTA 0: the chunk's validity words are written
+  kStaged = kMaskFull + 4,          // [4] CTA 0: a message is staged
+  kStageFree = kStaged + kStages,   // [4] CTA 0: its copy has landed in CTA 1
+  kPvDone = kStageFree + kStages,   // [3] both: the product of a message is complete
+  kVFull = kPvDone + kPBufs,        // [5] CTA 1
+  kVEmpty = kVFull + kVSlots,       // [5] CTA 1
+  kPFull = kVEmpty + kVSlots,       // [3] CTA 1: a message has landed
+  kReady = kPFull + kPBufs,         // [3] CTA 1: O is rescaled, the tiles' tails are zero
+  kDrain = kReady + kPBufs,
+  kNumBar
+};
+constexpr int kMiscOff = kBarOff + kNumBar * 8;
+struct Misc {
+  int tmem_base, abort, first_row, pad;
+  int64_t first_unit, total_units;
+  int64_t warp_sum[kThreads / 32];
+};
+constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kBarOff % 8 == 0 && kMiscOff % 8 == 0 && kMsgBytes % 16 == 0 && kStageOff % 128 == 0 && kPOff % 128 == 0, "alignment");
+constexpr int kTmemCols = 512;
+constexpr uint32_t kTmemS = 256;  // CTA 0: query blocks 0-7 in [0, 256), S buffers at 256 and 384
+constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk);
+constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
+
+// A row that part boundaries cut, as the combine kernel sees it.
+struct CutRow {
+  int row;    // -1: none
+  int first;  // cluster of its first partial
+  int count;  // partials, one per cluster from `first` on
+  int pad;
+};
+
+struct PagedMlaParams {
+  const __nv_bfloat16* q;
+  PagePool pool;
+  const int32_t* lens;
+  int n_rows, T, H, n_clusters;
+  int box;           // rows per TMA box
+  float scale_log2;
+  void* out;
+  int out_bf16;
+  float* lse;
+  CutRow* cut;       // [n_clusters]
+  float* part_ml;    // [2 * n_clusters][H][2]
+  float* part_o;     // [2 * n_clusters][H][512], unnormalised
+  int32_t* status;
+  int debug_stall;
+  uint64_t wait_limit_ns;
+};
+
+// Slots row r sees.
+__device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool& bad) {
+  const int b = r / p.T;
+  const int32_t len = checked_len(__ldg(p.lens + b), pool_capacity(p.pool), bad);
+  return max(0, len - p.T + (r - b * p.T) + 1);
+}
+__device__ __forceinline__ int64_t n_chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
+
+// One after the other, the parts of rows that fall to this cluster.  Every
+// role of both CTAs walks the same list.
+struct Walk {
+  int64_t u;       // first unit of row r
+  int64_t w0, w1;  // this cluster's units
+  int r, n_rows;
+  // of the current part:
+  int row, lo, hi, chunks;
+  int32_t len;
+  bool bad;
+
+  __device__ __forceinline__ bool next(const PagedMlaParams& p) {
+    while (r < n_rows && u < w1) {
+      len = row_len(p, r, bad);
+      const int64_t c = n_chunks_of(len), u0 = u + kRowUnits;
+      row = r;
+      chunks = (int)c;
+      const bool starts_here = u >= w0;
+      lo = (int)min(max(w0 - u0, (int64_t)0), c);
+      hi = (int)min(max(w1 - u0, (int64_t)0), c);
+      ++r;
+      u = u0 + c;
+      if (lo < hi || (c == 0 && starts_here)) return true;
+    }
+    return false;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                     const PagedMlaParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + kBarOff + 8u * (uint32_t)i; };
+  Misc* misc = reinterpret_cast<Misc*>(smem + kMiscOff);
+  volatile int* abort = &misc->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t peer_abort = mapa_shared(sbase + kMiscOff + (uint32_t)offsetof(Misc, abort), rank ^ 1u);
+  auto give_up = [&]() {
+    *abort = 1;
+    st_cluster_u32(peer_abort, 1u);
+  };
+
+  // ---- prologue: barriers, TMEM
+  if (threadIdx.x == 0) misc->abort = 0;
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_kv);
+      mbar_init(bar(kQFull), 1 + kSoftmaxThreads + p.debug_stall);
+      for (int i = 0; i < kKSlots; ++i) {
+        mbar_init(bar(kKFull + i), 1);
+        mbar_init(bar(kKEmpty + i), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(kSFull + i), 1);
+        mbar_init(bar(kSEmpty + i), kSoftmaxThreads);
+      }
+      for (int i = 0; i < 4; ++i) mbar_init(bar(kMaskFull + i), 1);
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(bar(kStaged + i), 128);
+        mbar_init(bar(kStageFree + i), 1);
+      }
+      for (int i = 0; i < kPBufs; ++i) {
+        mbar_init(bar(kPvDone + i), 1);
+        mbar_init(bar(kPFull + i), 1);
+        mbar_init(bar(kReady + i), 128);
+      }
+      for (int i = 0; i < kVSlots; ++i) {
+        mbar_init(bar(kVFull + i), 1);
+        mbar_init(bar(kVEmpty + i), 1);
+      }
+      mbar_init(bar(kDrain), 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(sbase + kMiscOff + (uint32_t)offsetof(Misc, tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();  // lens, q and the cache may come from the previous kernel
+  allow_dependents_launch();
+
+  // ---- the units of all rows, and the row this cluster's part begins in
+  const int cl = blockIdx.x >> 1;
+  {
+    const int per = (p.n_rows + kThreads - 1) / kThreads;
+    const int r0 = min((int)threadIdx.x * per, p.n_rows), r1 = min(r0 + per, p.n_rows);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      mine += kRowUnits + n_chunks_of(row_len(p, r, bad));
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) misc->warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int64_t v = misc->warp_sum[w];
+      if (w < warp) before += v;
+      total += v;
+    }
+    const int64_t share = (total + p.n_clusters - 1) / p.n_clusters;
+    const int64_t w0 = share * cl;
+    if (threadIdx.x == 0) {
+      misc->total_units = total;
+      if (w0 >= total) misc->first_row = p.n_rows;
+    }
+    if (before <= w0 && w0 < before + mine) {  // one thread, if any
+      int64_t u = before;
+      for (int r = r0; r < r1; ++r) {
+        bool bad;
+        const int64_t c = n_chunks_of(row_len(p, r, bad));
+        if (w0 < u + kRowUnits + c) {
+          misc->first_row = r;
+          misc->first_unit = u;
+          break;
+        }
+        u += kRowUnits + c;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
+  const int64_t share = (misc->total_units + p.n_clusters - 1) / p.n_clusters;
+  Walk wk;
+  wk.w0 = share * cl;
+  wk.w1 = min(wk.w0 + share, misc->total_units);
+  wk.r = misc->first_row;
+  wk.n_rows = p.n_rows;
+  wk.u = wk.r < p.n_rows ? misc->first_unit : 0;
+
+  if (rank == 1 && threadIdx.x == kSendWarp * 32) {
+    // this cluster's boundary cuts a row: the boundary behind the row's first
+    // partial describes the row to the combine kernel
+    CutRow c{-1, 0, 0, 0};
+    if (wk.r < p.n_rows) {
+      bool bad;
+      const int64_t n = n_chunks_of(row_len(p, wk.r, bad)), u0 = wk.u + kRowUnits;
+      if (wk.w0 > u0 && wk.w0 - share <= u0) {
+        c.row = wk.r;
+        c.first = (int)(u0 / share);
+        c.count = (int)((u0 + n - 1) / share) - c.first + 1;
+      }
+    }
+    p.cut[cl] = c;
+  }
+  // every barrier of both CTAs is initialised before either touches the other
+  cluster_sync_all();
+  const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const int nbox64 = kSub / p.box;  // boxes per 64 slots
+  const int64_t pool_rows = p.pool.n_pages * p.pool.page_size;
+
+  if (rank == 0) {
+    // ================================================================ QK side
+    if (warp == kLoadWarp) {
+      // ---- the chunks' blocks: lane i < 2 * nbox64 loads box i of a block
+      uint32_t g = 0, ring = 0;  // chunk and block counters over all parts
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        if (wk.bad && lane == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
+        const int b = wk.row / p.T;
+        const int nbox = 2 * nbox64;
+        // row coordinate and valid slots of this lane's box of chunk i
+        auto locate = [&](int i, int32_t& y, int& valid) {
+          const int64_t s = (int64_t)i * kChunk + lane * p.box;
+          valid = 0;
+          y = (int32_t)pool_rows;
+          if (lane < nbox && s < wk.len) {
+            const int64_t row = pool_row(p.pool, b, (int32_t)s);
+            if (row >= 0) {
+              y = (int32_t)row;
+              valid = min(p.box, wk.len - (int32_t)s);
+            } else {
+              report(p.status, DSA_ERR_BAD_INDEX);
+            }
+          }
+        };
+        int32_t y = 0, y_next = 0;
+        int valid = 0, valid_next = 0;
+        if (wk.lo < wk.hi) locate(wk.lo, y, valid);
+        for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
+          // validity words of the chunk, 16 slots (never more than a box) at a time
+          uint32_t word = 0;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int k0 = 32 * (lane & 3) + 16 * hh, bx = k0 / p.box;
+            const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
+            word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
+          }
+          if (lane < 4) reinterpret_cast<uint32_t*>(smem + kMaskOff)[4 * (g & 3) + lane] = word;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
+          if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
+#pragma unroll 1
+          for (int kb = 0; kb < kKB; ++kb, ++ring) {
+            const uint32_t slot = ring % kKSlots;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + slot), kKBlockBytes);
+            __syncwarp();
+            if (lane < nbox)
+              tma_load_2d(sbase + kKRingOff + slot * kKBlockBytes + lane * p.box * 128, &tm_kv, kb * 64, y, bar(kKFull + slot));
+          }
+          y = y_next;
+          valid = valid_next;
+        }
+      }
+      if (*abort) {
+        give_up();
+        volatile int never = 0;  // the loads in flight must land before the CTA exits
+        for (uint32_t k = ring > kKSlots ? ring - kKSlots : 0; k < ring; ++k)
+          mbar_wait(bar(kKFull + k % kKSlots), (k / kKSlots) & 1, &never, 10000000ull);
+      }
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        // ---- S(g) = Q . K(g)^T into buffer g & 1
+        const uint64_t q8 = smem_desc(sbase + kQ8Off, 16, 1024, kSwizzle128B);
+        const uint64_t kb0 = smem_desc(sbase + kKRingOff, 16, 1024, kSwizzle128B);
+        uint32_t g = 0, ring = 0, item = 0;
+        bool ok = true;
+        while (ok && wk.next(p)) {
+          if (wk.lo >= wk.hi) continue;
+          if (!(ok = mbar_wait(bar(kQFull), item & 1, abort, p.wait_limit_ns))) break;
+          ++item;
+          tc_fence_after();
+          for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
+            const int sb = g & 1;
+            if (g >= 2 && !(ok = mbar_wait(bar(kSEmpty + sb), ((g - 2) >> 1) & 1, abort, p.wait_limit_ns))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + kTmemS + 128 * sb;
+#pragma unroll 1
+            for (int kb = 0; kb < kKB; ++kb, ++ring) {
+              const uint32_t slot = ring % kKSlots;
+              if (!(ok = mbar_wait(bar(kKFull + slot), (ring / kKSlots) & 1, abort, p.wait_limit_ns))) break;
+              tc_fence_after();
+              const uint64_t bs = kb0 + (uint64_t)((slot * kKBlockBytes) >> 4);
+              if (kb < kKB - 1) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_f16_ts(d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
+              } else {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_f16_ss(d, q8 + (uint64_t)ks * 2, bs + (uint64_t)ks * 2, kIdescQK, 1u);
+              }
+              tc_commit(bar(kKEmpty + slot));
+            }
+            if (!ok) break;
+            tc_commit(bar(kSFull + sb));
+          }
+        }
+        if (*abort) {
+          give_up();
+          volatile int never = 0;  // tensor-core work ends before TMEM is released
+          tc_commit(bar(kDrain));
+          mbar_wait(bar(kDrain), 0, &never, 10000000ull);
+        }
+      }
+    } else if (warp == kSendWarp) {
+      if (lane == 0) {
+        // ---- message j (64 slots of P, alpha, l, m) to CTA 1's buffer j % 3
+        const uint32_t rem_msg = mapa_shared(sbase + kPOff, 1);
+        const uint32_t rem_pfull = mapa_shared(bar(kPFull), 1);
+        uint32_t j = 0;
+        bool ok = true;
+        while (ok && wk.next(p)) {
+          for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
+            const uint32_t st = j % kStages, pb = j % kPBufs;
+            if (!(ok = mbar_wait(bar(kStaged + st), (j / kStages) & 1, abort, p.wait_limit_ns))) break;
+            if (j >= kPBufs &&
+                !(ok = mbar_wait_cluster(bar(kPvDone + pb), ((j / kPBufs) - 1) & 1, abort, p.wait_limit_ns))) break;
+            mbar_arrive_expect_tx_cluster(rem_pfull + 8u * pb, kMsgBytes);
+            bulk_copy_s2c(rem_msg + pb * kMsgBytes, sbase + kStageOff + st * kMsgBytes, kMsgBytes, rem_pfull + 8u * pb);
+          }
+        }
+        // CTA 1's last arrivals here must land before this CTA exits
+        for (uint32_t k = j > kPBufs ? j - kPBufs : 0; ok && k < j; ++k)
+          ok = mbar_wait_cluster(bar(kPvDone + k % kPBufs), (k / kPBufs) & 1, abort, p.wait_limit_ns);
+        if (*abort) {
+          give_up();
+          volatile int never = 0;  // the copies must have left the staging buffers
+          for (uint32_t k = j > kStages ? j - kStages : 0; k < j; ++k)
+            mbar_wait_cluster(bar(kStageFree + k % kStages), (k / kStages) & 1, &never, 10000000ull);
+        }
+      }
+    } else if (warp < 8) {
+      // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
+      const int h = (warp & 3) * 32 + lane, half = warp >> 2;
+      const bool dead = (warp & 3) * 32 >= p.H;  // a warp without heads only keeps step
+      uint32_t g = 0, item = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        if (wk.lo >= wk.hi) continue;
+        ++item;
+        {  // the query: every product with the one before is complete (its S was read)
+          if (threadIdx.x == 0) {
+            mbar_arrive_expect_tx(bar(kQFull), kKBlockBytes);
+            tma_load_2d(sbase + kQ8Off, &tm_q, 8 * 64, wk.row * p.H, bar(kQFull));
+          }
+          const bool live = h < p.H;
+          const uint4* qrow = reinterpret_cast<const uint4*>(p.q + ((int64_t)wk.row * p.H + (live ? h : 0)) * kDQK) + 32 * half;
+#pragma unroll 2
+          for (int kb = 0; kb < 4; ++kb) {
+            uint32_t w[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint4 v = live ? __ldg(qrow + 8 * kb + u) : make_uint4(0u, 0u, 0u, 0u);
+              w[4 * u] = v.x;
+              w[4 * u + 1] = v.y;
+              w[4 * u + 2] = v.z;
+              w[4 * u + 3] = v.w;
+            }
+            tmem_st32(lane_addr + 32 * (4 * half + kb), w);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kQFull));
+        }
+        float m_run = -INFINITY, l_run = 0.f;
+        for (int i = wk.lo; i < wk.hi; ++i, ++g) {
+          const int sb = g & 1;
+          const uint32_t j = 2 * g + half, stg = j % kStages;
+          ok = mbar_wait(bar(kMaskFull + (g & 3)), (g >> 2) & 1, abort, p.wait_limit_ns) &&
+               mbar_wait(bar(kSFull + sb), (g >> 1) & 1, abort, p.wait_limit_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          uint32_t sv[64];
+          float mx = -INFINITY;
+          if (ok) {
+            tc_fence_after();
+            if (!dead) {
+              tmem_ld64(lane_addr + kTmemS + 128 * sb + 64 * half, sv);
+              tc_wait_ld();
+            }
+            tc_fence_before();
+            const uint32_t* vm = reinterpret_cast<const uint32_t*>(smem + kMaskOff) + 4 * (g & 3) + 2 * half;
+            const uint32_t vm0 = vm[0], vm1 = vm[1];
+            mbar_arrive(bar(kSEmpty + sb));
+            if (!dead) {
+              // x = s * scale * log2(e); masked slots -inf
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) {
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                                            make_float2(p.scale_log2, p.scale_log2));
+                sv[c] = __float_as_uint(x.x);
+                sv[c + 1] = __float_as_uint(x.y);
+              }
+              if ((vm0 & vm1) != ~0u) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  if (!((vm0 >> c) & 1u)) sv[c] = 0xff800000u;
+                  if (!((vm1 >> c) & 1u)) sv[32 + c] = 0xff800000u;
+                }
+              }
+              float m8[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                m8[c] = __uint_as_float(sv[c]);
+#pragma unroll
+                for (int e = 8 + c; e < 64; e += 8) m8[c] = fmaxf(m8[c], __uint_as_float(sv[e]));
+              }
+              mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+              reinterpret_cast<float*>(smem + kMaxOff)[256 * sb + 128 * half + h] = mx;
+            }
+            // the staging buffer is free once the copy of message j - 4 has landed
+            if (g >= 2) ok = mbar_wait_cluster(bar(kStageFree + stg), ((j / kStages) - 1) & 1, abort, p.wait_limit_ns);
+          }
+          // both halves' maxima are written; all eight warps leave together
+          if (named_barrier_or(1, kSoftmaxThreads, !ok)) {
+            ok = false;
+            break;
+          }
+          uint8_t* const stage = smem + kStageOff + stg * kMsgBytes;
+          if (!dead) {
+            mx = fmaxf(mx, reinterpret_cast<const float*>(smem + kMaxOff)[256 * sb + 128 * (half ^ 1) + h]);
+            float alpha = 1.f;
+            if (mx > m_run + 8.f) {  // always in the row's first chunk that holds a finite score
+              alpha = exp2f(m_run - mx);  // 0 at first
+              m_run = mx;
+            }
+            const float sub = m_run == -INFINITY ? 0.f : m_run;
+            float2 l2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 nm = make_float2(-sub, -sub);
+            uint8_t* const prow = stage + (h >> 3) * 1024 + (h & 7) * 16;
+#pragma unroll
+            for (int c8 = 0; c8 < 8; ++c8) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = 8 * c8 + 2 * e;
+                const float2 d = __fadd2_rn(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), nm);
+                const float2 pv = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                l2[e] = __fadd2_rn(l2[e], pv);
+                const __nv_bfloat162 pb = __floats2bfloat162_rn(pv.x, pv.y);
+                w4[e] = *reinterpret_cast<const uint32_t*>(&pb);
+              }
+              *reinterpret_cast<uint4*>(prow + c8 * 128) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+            const float2 a = __fadd2_rn(l2[0], l2[1]), bb = __fadd2_rn(l2[2], l2[3]);
+            l_run = l_run * alpha + ((a.x + bb.x) + (a.y + bb.y));
+            float* const tail = reinterpret_cast<float*>(stage + kPBytes);
+            tail[h] = alpha;
+            tail[128 + h] = l_run;
+            tail[256 + h] = m_run;
+          } else {
+            reinterpret_cast<float*>(stage + kPBytes)[h] = 1.f;
+          }
+          fence_proxy_async_smem();  // the copy engine reads the message
+          mbar_arrive(bar(kStaged + stg));
+        }
+      }
+      if (*abort) {
+        give_up();
+        volatile int never = 0;  // block 8 of the query must land before the CTA exits
+        if (threadIdx.x == 0 && item > 0) mbar_wait(bar(kQFull), (item - 1) & 1, &never, 10000000ull);
+      }
+    }
+  } else {
+    // ================================================================ PV side
+    if (warp == kLoadWarp) {
+      // ---- 64-slot x 256-column tiles: lane i < 4 * nbox64 loads box
+      // i % nbox64 of column block i / nbox64
+      uint32_t ring = 0;
+      bool ok = true;
+      const int bx = lane % nbox64, blk = lane / nbox64;
+      while (ok && wk.next(p)) {
+        const int b = wk.row / p.T;
+        auto locate = [&](int i) -> int32_t {  // i counts 64-slot halves
+          const int64_t s = (int64_t)i * kSub + bx * p.box;
+          if (blk < 4 && s < wk.len) {
+            const int64_t row = pool_row(p.pool, b, (int32_t)s);
+            if (row >= 0) return (int32_t)row;
+          }
+          return (int32_t)pool_rows;
+        };
+        int32_t y = 0, y_next = 0;
+        if (wk.lo < wk.hi) y = locate(2 * wk.lo);
+        for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i) {
+          if (i + 1 < 2 * wk.hi) y_next = locate(i + 1);
+#pragma unroll
+          for (int n = 0; n < 2; ++n, ++ring) {
+            const uint32_t slot = ring % kVSlots;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kVEmpty + slot), ((ring / kVSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + slot), kVSlotBytes);
+            __syncwarp();
+            if (blk < 4)
+              tma_load_2d(sbase + slot * kVSlotBytes + blk * kVBlockBytes + bx * p.box * 128, &tm_kv, 256 * n + 64 * blk, y,
+                          bar(kVFull + slot));
+          }
+          y = y_next;
+        }
+      }
+      if (*abort) {
+        give_up();
+        volatile int never = 0;
+        for (uint32_t k = ring > kVSlots ? ring - kVSlots : 0; k < ring; ++k)
+          mbar_wait(bar(kVFull + k % kVSlots), (k / kVSlots) & 1, &never, 10000000ull);
+      }
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        // ---- O[:, 256 n ..] += P(j) . V(j)[:, 256 n ..]
+        const uint64_t pa0 = smem_desc(sbase + kPOff, 128, 1024, kSwizzleNone);
+        const uint64_t vb0 = smem_desc(sbase, kVBlockBytes, 1024, kSwizzle128B);
+        uint32_t j = 0, ring = 0;
+        bool ok = true;
+        while (ok && wk.next(p)) {
+          for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
+            const uint32_t pb = j % kPBufs;
+            if (!(ok = mbar_wait(bar(kReady + pb), (j / kPBufs) & 1, abort, p.wait_limit_ns))) break;
+            tc_fence_after();
+            const uint64_t ad = pa0 + (uint64_t)((pb * kMsgBytes) >> 4);
+#pragma unroll 1
+            for (int n = 0; n < 2; ++n, ++ring) {
+              const uint32_t slot = ring % kVSlots;
+              if (!(ok = mbar_wait(bar(kVFull + slot), (ring / kVSlots) & 1, abort, p.wait_limit_ns))) break;
+              tc_fence_after();
+              const uint64_t bd = vb0 + (uint64_t)((slot * kVSlotBytes) >> 4);
+#pragma unroll
+              for (int s = 0; s < kSub / 16; ++s)
+                mma_f16_ss(tmem + 256 * n, ad + (uint64_t)((s * 256) >> 4), bd + (uint64_t)((s * 2048) >> 4), kIdescPV,
+                           (i > 2 * wk.lo || s > 0) ? 1u : 0u);
+              tc_commit(bar(kVEmpty + slot));
+            }
+            if (!ok) break;
+            tc_commit_mc(bar(kPvDone + pb), 0x3);
+          }
+        }
+        if (*abort) {
+          give_up();
+          volatile int never = 0;
+          tc_commit(bar(kDrain));
+          mbar_wait(bar(kDrain), 0, &never, 10000000ull);
+        }
+      }
+    } else if (warp < 4) {
+      // ---- rescale and epilogue: thread h owns O row h (TMEM lane h)
+      const int h = threadIdx.x;
+      const bool dead = warp * 32 >= p.H;
+      const uint32_t rem_stage_free = mapa_shared(bar(kStageFree), 0);
+      uint8_t* const ostage = smem + kOutOff + warp * 2048;
+      uint32_t j = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        float l_half[2] = {0.f, 0.f}, m_row = -INFINITY;
+        for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
+          const uint32_t pb = j % kPBufs;
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(kPFull + pb), (j / kPBufs) & 1, abort, p.wait_limit_ns));
+          if (!ok) break;
+          const float* tail = reinterpret_cast<const float*>(smem + kPOff + pb * kMsgBytes + kPBytes);
+          if (!dead) {
+            const float alpha = (i & 1) ? 1.f : tail[h];  // a chunk's factor comes with its first half
+            if (i & 1) l_half[1] = tail[128 + h];
+            else l_half[0] = tail[128 + h];
+            m_row = tail[256 + h];
+            if (i > 2 * wk.lo && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // every product so far is complete when the last one is
+              ok = __all_sync(0xffffffffu, mbar_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cb = 0; cb < kDV / 32; ++cb) {
+                uint32_t ov[32];
+                tmem_ld32(lane_addr + 32 * cb, ov);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+                tmem_st32(lane_addr + 32 * cb, ov);
+              }
+              tc_wait_st();
+            }
+          }
+          // slots behind the row's end that share the last box with it
+          const int64_t left = (int64_t)wk.len - (int64_t)i * kSub;
+          if (left > 0 && left < kSub && left % p.box != 0) {
+            const int z0 = (int)left, z1 = ((int)left + p.box - 1) / p.box * p.box;
+#pragma unroll
+            for (uint32_t n = 0; n < 2; ++n) {
+              const uint32_t k = 2 * j + n, slot = k % kVSlots;
+              ok = ok && mbar_wait(bar(kVFull + slot), (k / kVSlots) & 1, abort, p.wait_limit_ns);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              for (int e = threadIdx.x; e < (z1 - z0) * 32; e += 128) {  // 4 blocks x 8 pieces of 16 bytes per slot
+                const int z = z0 + (e >> 5), blk = (e >> 3) & 3, c = e & 7;
+                *reinterpret_cast<uint4*>(smem + slot * kVSlotBytes + blk * kVBlockBytes + z * 128 + c * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+            if (!ok) break;
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(bar(kReady + pb));
+          if (h == 0) mbar_arrive_cluster(rem_stage_free + 8u * (j % kStages));
+        }
+        if (!ok) break;
+        const bool any = wk.lo < wk.hi;
+        if (any)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns));
+        if (!ok) break;
+        if (dead) continue;
+        tc_fence_after();
+        const float l = l_half[0] + l_half[1];
+        const bool whole = wk.hi - wk.lo == wk.chunks;
+        const float mul = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
+        const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
+        const bool as_bf16 = whole && p.out_bf16;
+        // 64 bytes of 32 rows at a time through shared memory, so that four
+        // lanes write a row's piece
+        uint8_t* const rowp = ostage + lane * 64;
+        const int sw = (lane >> 1) & 3;
+        const int64_t row_bytes = as_bf16 ? kDV * 2 : kDV * 4;
+        uint8_t* const gout = whole ? reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.row * p.H + warp * 32) * row_bytes
+                                    : reinterpret_cast<uint8_t*>(p.part_o) + (part * p.H + warp * 32) * row_bytes;
+        auto flush = [&](int64_t col_byte) {
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int rr = 8 * u + (lane >> 2), c = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+            if (warp * 32 + rr < p.H) *reinterpret_cast<uint4*>(gout + rr * row_bytes + col_byte + 16 * c) = v;
+          }
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int cb = 0; cb < kDV / 32; ++cb) {
+          uint32_t ov[32];
+          if (any) {
+            tmem_ld32(lane_addr + 32 * cb, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] = l == 0.f && whole ? 0u : __float_as_uint(__uint_as_float(ov[c]) * mul);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] = 0u;
+          }
+          if (as_bf16) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 t2 =
+                    __floats2bfloat162_rn(__uint_as_float(ov[8 * c + 2 * e]), __uint_as_float(ov[8 * c + 2 * e + 1]));
+                w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+              }
+              *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+            flush(cb * 64);
+          } else {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) =
+                    make_uint4(ov[16 * hf + 4 * c], ov[16 * hf + 4 * c + 1], ov[16 * hf + 4 * c + 2], ov[16 * hf + 4 * c + 3]);
+              flush(cb * 128 + hf * 64);
+            }
+          }
+        }
+        tc_fence_before();  // O is read: the next row's first product (after Ready) may overwrite it
+        if (h < p.H) {
+          if (whole) {
+            if (p.lse) p.lse[(int64_t)wk.row * p.H + h] = l == 0.f ? -INFINITY : (m_row + log2f(l)) * 0.69314718055994531f;
+          } else {
+            p.part_ml[2 * (part * p.H + h)] = m_row;
+            p.part_ml[2 * (part * p.H + h) + 1] = l;
+          }
+        }
+      }
+      if (*abort) give_up();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves while the other may still write into its shared memory
+  cluster_sync_all();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort) report(p.status, DSA_ERR_TIMEOUT);
+}
+
+// Joins the partials of the cut rows: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// One CTA per (cut row, head), in turn; thread = (four columns, half of the partials).
+constexpr int kCombineThreads = 256;
+constexpr int kMaxClusters = 128;
+
+__global__ void __launch_bounds__(kCombineThreads)
+    paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
+                             const float* __restrict__ part_o, int n_clusters, int H, void* out, int out_bf16, float* lse) {
+  __shared__ CutRow s_cut[kMaxClusters];
+  __shared__ int s_n;
+  __shared__ float s_w[kMaxClusters], s_ml[2];
+  __shared__ float4 s_half[128];
   grid_dependency_wait();
   allow_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (H + kHeads - 1) / kHeads;
-  const int r = blockIdx.x / groups, h = (blockIdx.x % groups) * kHeads + warp;
-  const int b = r / T, t = r - b * T;
-  bool bad;
-  const int32_t len = checked_len(lens[b], pool_capacity(pool), bad);
-  if (bad && threadIdx.x == 0) report(status, DSA_ERR_BAD_OFFSETS);
-  const int L = max(0, len - T + t + 1);
-  const int64_t rh = (int64_t)r * H + h;
-  if (h < H)
-    for (int c = lane; c < kDQK; c += 32) sq[warp * kDQK + c] = __bfloat162float(q[rh * kDQK + c]);
-  float m = -INFINITY, l = 0.f, o[16];
-  for (int c = 0; c < 16; ++c) o[c] = 0.f;
-  for (int s0 = 0; s0 < L; s0 += kTile) {
-    __syncthreads();
-    for (int i = warp; i < kTile; i += 8) {
-      const int64_t row = s0 + i < L ? pool_row(pool, b, s0 + i) : -1;
-      if (lane == 0) {
-        s_ok[i] = row >= 0;
-        if (row < 0 && s0 + i < L) report(status, DSA_ERR_BAD_INDEX);
+  if (warp == 0) {
+    int n = 0;
+    for (int c0 = 0; c0 < n_clusters; c0 += 32) {
+      CutRow c{-1, 0, 0, 0};
+      if (c0 + lane < n_clusters) c = cut[c0 + lane];
+      const uint32_t m = __ballot_sync(0xffffffffu, c.row >= 0);
+      if (c.row >= 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = c;
+      n += __popc(m);
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int tasks = s_n * H;
+  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const CutRow c = s_cut[task / H];
+    const int h = task % H;
+    // the first partial is its cluster's second, the others are their clusters' first
+    auto part = [&](int i) -> int64_t { return ((int64_t)2 * (c.first + i) + (i == 0 ? 1 : 0)) * H + h; };
+    if (warp == 0) {
+      float M = -INFINITY;
+      for (int i = lane; i < c.count; i += 32) M = fmaxf(M, part_ml[2 * part(i)]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float sub = M == -INFINITY ? 0.f : M;
+      float l = 0.f;
+      for (int i = lane; i < c.count; i += 32) {
+        const float w = exp2f(part_ml[2 * part(i)] - sub);
+        s_w[i] = w;
+        l += w * part_ml[2 * part(i) + 1];
       }
-      uint4* d = reinterpret_cast<uint4*>(tile + i * kRowPad);
-      for (int c = lane; c < kDQK / 8; c += 32)
-        d[c] = row >= 0 ? reinterpret_cast<const uint4*>(kv + row * kDQK)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        s_ml[0] = M;
+        s_ml[1] = l;
+      }
     }
     __syncthreads();
-    float x = 0.f;
-    const __nv_bfloat16* k = tile + lane * kRowPad;
-    for (int c = 0; c < kDQK; c += 2) {
-      const float2 kk = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(k + c));
-      x = fmaf(kk.x, sq[warp * kDQK + c], x);
-      x = fmaf(kk.y, sq[warp * kDQK + c + 1], x);
+    const int c4 = threadIdx.x & 127, hf = threadIdx.x >> 7;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = hf; i < c.count; i += 2) {
+      const float w = s_w[i];
+      const float4 o = __ldg(reinterpret_cast<const float4*>(part_o + part(i) * kDV) + c4);
+      if (w != 0.f) {  // a partial without any visible slot holds nothing
+        a.x = fmaf(w, o.x, a.x);
+        a.y = fmaf(w, o.y, a.y);
+        a.z = fmaf(w, o.z, a.z);
+        a.w = fmaf(w, o.w, a.w);
+      }
     }
-    x = s_ok[lane] ? x * scale_log2 : -INFINITY;
-    float mx = x;
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    const float m_new = fmaxf(m, mx), sub = m_new == -INFINITY ? 0.f : m_new;
-    const float p = exp2f(x - sub), a = exp2f(m - sub);
-    float ps = p;
-    for (int d = 16; d; d >>= 1) ps += __shfl_xor_sync(~0u, ps, d);
-    l = l * a + ps;
-    m = m_new;
-    for (int c = 0; c < 16; ++c) o[c] *= a;
-    for (int j = 0; j < kTile; ++j) {
-      const float pj = __shfl_sync(~0u, p, j);
-      for (int c = 0; c < 16; ++c) o[c] = fmaf(pj, __bfloat162float(tile[j * kRowPad + 32 * c + lane]), o[c]);
+    if (hf == 1) s_half[c4] = a;
+    __syncthreads();
+    if (hf == 0) {
+      const float4 o = s_half[c4];
+      const float l = s_ml[1], inv = l == 0.f ? 0.f : 1.f / l;
+      a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4((a.x + o.x) * inv, (a.y + o.y) * inv, (a.z + o.z) * inv, (a.w + o.w) * inv);
+      const int64_t rh = (int64_t)c.row * H + h;
+      if (out_bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
+        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[c4] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      } else {
+        reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + rh * kDV)[c4] = a;
+      }
+      if (c4 == 0 && lse) lse[rh] = l == 0.f ? -INFINITY : (s_ml[0] + log2f(l)) * 0.69314718055994531f;
     }
+    __syncthreads();
   }
-  if (h >= H) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
-  for (int c = 0; c < 16; ++c) {
-    if (out_bf16) reinterpret_cast<__nv_bfloat16*>(out)[rh * kDV + 32 * c + lane] = __float2bfloat16(o[c] * inv);
-    else reinterpret_cast<float*>(out)[rh * kDV + 32 * c + lane] = o[c] * inv;
-  }
-  if (lse && lane == 0) lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Clusters of a launch: as many as the card runs at once.
+int paged_clusters() {
+  static PerDeviceOnce once;
+  static int count[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const int half = std::max(1, std::min(device_info().sm_count / 2, kMaxClusters));
+  if (dev < 0 || dev >= 64) return half;
+  const cudaError_t e = once.run([&] {
+    cudaError_t e2 = cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e2 != cudaSuccess) return e2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * half);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e2 = cudaOccupancyMaxActiveClusters(&n, paged_mla_kernel, &cfg);
+    if (e2 != cudaSuccess) return e2;
+    count[dev] = std::max(1, std::min(n, half));
+    return cudaSuccess;
+  });
+  return e == cudaSuccess ? count[dev] : half;
+}
+
+size_t paged_workspace(int H) {
+  const size_t n = (size_t)paged_clusters();
+  return n * sizeof(CutRow) + 2 * n * H * 2 * sizeof(float) + 2 * n * H * kDV * sizeof(float);
 }
 
 }  // namespace
@@ -90,8 +922,8 @@ using namespace dsa;
 extern "C" {
 
 size_t dsa_paged_mla_workspace_size(int B, int T, int H) {
-  (void)B, (void)T, (void)H;
-  return 0;
+  if (B <= 0 || T <= 0 || (int64_t)B * T > (int64_t)1 << 24 || H < 1 || H > DSA_MAX_HEADS) return 0;
+  return paged_workspace(H);
 }
 
 int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,
@@ -102,21 +934,44 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_INVALID_ARG;
   if (!(scale == scale) || !is_aligned16(q) || !is_aligned16(out)) return DSA_ERR_INVALID_ARG;
-  const size_t need = dsa_paged_mla_workspace_size(B, T, H);
-  if (need > 0 && (!workspace || ws_bytes < need || !is_aligned16(workspace))) return DSA_ERR_WORKSPACE;
-  const PagePool pool{page_table, ld_table, n_pages, max_pages, page_size};
-  constexpr int kSmem = kTile * kRowPad * 2 + kHeads * kDQK * 4;
-  static PerDeviceOnce attr;
-  if (attr.run([] {
-        return cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-      }) != cudaSuccess)
+  const size_t need = paged_workspace(H);
+  if (!workspace || ws_bytes < need || !is_aligned16(workspace)) return DSA_ERR_WORKSPACE;
+  MlaParams debug;
+  take_attention_debug(debug);
+  const int n = paged_clusters();
+  PagedMlaParams p;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.pool = PagePool{page_table, ld_table, n_pages, max_pages, page_size};
+  p.lens = lens;
+  p.n_rows = B * T;
+  p.T = T;
+  p.H = H;
+  p.n_clusters = n;
+  p.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out;
+  p.out_bf16 = out_dtype == DSA_BF16 ? 1 : 0;
+  p.lse = lse;
+  p.cut = reinterpret_cast<CutRow*>(workspace);
+  p.part_o = reinterpret_cast<float*>(p.cut + n);
+  p.part_ml = p.part_o + (size_t)2 * n * H * kDV;
+  p.status = dev_status;
+  p.debug_stall = debug.debug_stall;
+  p.wait_limit_ns = debug.wait_limit_ns;
+  CUtensorMap tq, tkv;
+  if (!make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tkv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)n_pages * page_size, kDQK * 2, 64,
+                    (uint32_t)p.box, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
-  const unsigned grid = (unsigned)B * T * ((H + kHeads - 1) / kHeads);
-  const cudaError_t e = launch_pdl(paged_mla_kernel, dim3(grid), dim3(256), kSmem, reinterpret_cast<cudaStream_t>(stream),
-                                   reinterpret_cast<const __nv_bfloat16*>(q),
-                                   reinterpret_cast<const __nv_bfloat16*>(kv_pages), pool, lens, T, H,
-                                   scale * 1.4426950408889634f, out, out_dtype == DSA_BF16 ? 1 : 0, lse, dev_status);
-  return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tkv, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const unsigned grid = (unsigned)std::min<int64_t>((int64_t)(n - 1) * H, 8 * (int64_t)device_info().sm_count);
+  if (n > 1 && launch_pdl(paged_mla_combine_kernel, dim3(grid), dim3(kCombineThreads), 0, s, (const CutRow*)p.cut,
+                          (const float*)p.part_ml, (const float*)p.part_o, n, H, out, p.out_bf16, lse) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
 }
 
 }  // extern "C"
