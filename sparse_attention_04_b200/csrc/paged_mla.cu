@@ -73,13 +73,14 @@ constexpr int kVBlockBytes = kSub * 128;            // 64 slots x 64 columns
 constexpr int kVSlots = 5;
 constexpr int kPBufs = 3;
 constexpr int kPOff = kVSlots * kVSlotBytes;                      // 163840
-constexpr int kOutOff = kPOff + kPBufs * (int)kMsgBytes;          // 217600: epilogue staging, 2 KB per warp
-constexpr int kPvEnd = kOutOff + 4 * 2048;
+constexpr int kOutOff = kPOff + kPBufs * (int)kMsgBytes;          // 217600: epilogue staging, 1 KB per warp
+constexpr int kPvEnd = kOutOff + 8 * 1024;
 // ---- both
 constexpr int kBarOff = (kQkEnd > kPvEnd ? kQkEnd : kPvEnd);
 enum Bar : int {
-  kQFull = 0,
-  kKFull = 1,                       // [8] CTA 0
+  kQFull = 0,                       // CTA 0: query block 8 has landed
+  kQFree,                           // CTA 0: the products of a part are complete
+  kKFull,                           // [8] CTA 0
   kKEmpty = kKFull + kKSlots,       // [8] CTA 0
   kSFull = kKEmpty + kKSlots,       // [2] CTA 0
   kSEmpty = kSFull + 2,             // [2] CTA 0
@@ -127,8 +128,8 @@ struct PagedMlaParams {
   int out_bf16;
   float* lse;
   CutRow* cut;       // [n_clusters]
-  float* part_ml;    // [2 * n_clusters][H][2]
-  float* part_o;     // [2 * n_clusters][H][512], unnormalised
+  float* part_ml;    // [2 * n_clusters][2][H]: maximum, sum
+  float* part_o;     // [2 * n_clusters][128][H][4], unnormalised
   int32_t* status;
   int debug_stall;
   uint64_t wait_limit_ns;
@@ -192,7 +193,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&tm_kv);
-      mbar_init(bar(kQFull), 1 + kSoftmaxThreads + p.debug_stall);
+      mbar_init(bar(kQFull), 1 + p.debug_stall);
+      mbar_init(bar(kQFree), 1);
       for (int i = 0; i < kKSlots; ++i) {
         mbar_init(bar(kKFull + i), 1);
         mbar_init(bar(kKEmpty + i), 1);
@@ -209,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPBufs; ++i) {
         mbar_init(bar(kPvDone + i), 1);
         mbar_init(bar(kPFull + i), 1);
-        mbar_init(bar(kReady + i), 128);
+        mbar_init(bar(kReady + i), 256);
       }
       for (int i = 0; i < kVSlots; ++i) {
         mbar_init(bar(kVFull + i), 1);
@@ -222,7 +224,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc(sbase + kMiscOff + (uint32_t)offsetof(Misc, tmem_base), kTmemCols);
     tmem_relinquish();
   }
-  grid_dependency_wait();  // lens, q and the cache may come from the previous kernel
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive_release();  // the barriers are initialised; waited for before the partner's are touched
+  grid_dependency_wait();    // lens, q and the cache may come from the previous kernel
   allow_dependents_launch();
 
   // ---- the units of all rows, and the row this cluster's part begins in
@@ -269,9 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
   const int64_t share = (misc->total_units + p.n_clusters - 1) / p.n_clusters;
   Walk wk;
@@ -296,8 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     p.cut[cl] = c;
   }
-  // every barrier of both CTAs is initialised before either touches the other
-  cluster_sync_all();
+  cluster_wait_acquire();
   const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const int nbox64 = kSub / p.box;  // boxes per 64 slots
   const int64_t pool_rows = p.pool.n_pages * p.pool.page_size;
@@ -306,10 +309,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ================================================================ QK side
     if (warp == kLoadWarp) {
       // ---- the chunks' blocks: lane i < 2 * nbox64 loads box i of a block
-      uint32_t g = 0, ring = 0;  // chunk and block counters over all parts
+      uint32_t g = 0, ring = 0, item = 0;  // chunk, block and part counters
       bool ok = true;
       while (ok && wk.next(p)) {
         if (wk.bad && lane == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
+        if (wk.lo >= wk.hi) continue;
         const int b = wk.row / p.T;
         const int nbox = 2 * nbox64;
         // row coordinate and valid slots of this lane's box of chunk i
@@ -329,7 +333,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         };
         int32_t y = 0, y_next = 0;
         int valid = 0, valid_next = 0;
-        if (wk.lo < wk.hi) locate(wk.lo, y, valid);
+        locate(wk.lo, y, valid);
+        // the query's blocks 0-7 go through the ring, on their way to TMEM
+#pragma unroll 1
+        for (int kb = 0; kb < kKB - 1; ++kb, ++ring) {
+          const uint32_t slot = ring % kKSlots;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kKFull + slot), kKBlockBytes);
+            tma_load_2d(sbase + kKRingOff + slot * kKBlockBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + slot));
+          }
+        }
+        if (!ok) break;
+        if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns)))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kQFull), kKBlockBytes);
+          tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.row * p.H, bar(kQFull));
+        }
+        ++item;
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           // validity words of the chunk, 16 slots (never more than a box) at a time
           uint32_t word = 0;
@@ -361,47 +382,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         volatile int never = 0;  // the loads in flight must land before the CTA exits
         for (uint32_t k = ring > kKSlots ? ring - kKSlots : 0; k < ring; ++k)
           mbar_wait(bar(kKFull + k % kKSlots), (k / kKSlots) & 1, &never, 10000000ull);
+        if (item > 0) mbar_wait(bar(kQFull), (item - 1) & 1, &never, 10000000ull);
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        // ---- S(g) = Q . K(g)^T into buffer g & 1
-        const uint64_t q8 = smem_desc(sbase + kQ8Off, 16, 1024, kSwizzle128B);
-        const uint64_t kb0 = smem_desc(sbase + kKRingOff, 16, 1024, kSwizzle128B);
-        uint32_t g = 0, ring = 0, item = 0;
-        bool ok = true;
-        while (ok && wk.next(p)) {
-          if (wk.lo >= wk.hi) continue;
-          if (!(ok = mbar_wait(bar(kQFull), item & 1, abort, p.wait_limit_ns))) break;
-          ++item;
-          tc_fence_after();
-          for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
-            const int sb = g & 1;
-            if (g >= 2 && !(ok = mbar_wait(bar(kSEmpty + sb), ((g - 2) >> 1) & 1, abort, p.wait_limit_ns))) break;
-            tc_fence_after();
-            const uint32_t d = tmem + kTmemS + 128 * sb;
+      // ---- S(g) = Q . K(g)^T into buffer g & 1
+      const uint32_t on = elect_one();
+      const uint64_t q8 = smem_desc(sbase + kQ8Off, 16, 1024, kSwizzle128B);
+      const uint64_t kb0 = smem_desc(sbase + kKRingOff, 16, 1024, kSwizzle128B);
+      auto wait = [&](int which, uint32_t parity) {
+        const bool there = __all_sync(0xffffffffu, mbar_wait(bar(which), parity, abort, p.wait_limit_ns));
+        tc_fence_after();
+        return there;
+      };
+      uint32_t g = 0, ring = 0, item = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        if (wk.lo >= wk.hi) continue;
+        // the query into TMEM, once no product reads the one before
+        if (item > 0 && !(ok = wait(kQFree, (item - 1) & 1))) break;
 #pragma unroll 1
-            for (int kb = 0; kb < kKB; ++kb, ++ring) {
-              const uint32_t slot = ring % kKSlots;
-              if (!(ok = mbar_wait(bar(kKFull + slot), (ring / kKSlots) & 1, abort, p.wait_limit_ns))) break;
-              tc_fence_after();
-              const uint64_t bs = kb0 + (uint64_t)((slot * kKBlockBytes) >> 4);
-              if (kb < kKB - 1) {
+        for (int kb = 0; kb < kKB - 1; ++kb, ++ring) {
+          const uint32_t slot = ring % kKSlots;
+          if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
+          if (on) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_f16_ts(d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
-              } else {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_f16_ss(d, q8 + (uint64_t)ks * 2, bs + (uint64_t)ks * 2, kIdescQK, 1u);
-              }
-              tc_commit(bar(kKEmpty + slot));
-            }
-            if (!ok) break;
-            tc_commit(bar(kSFull + sb));
+            for (int ks = 0; ks < 4; ++ks)
+              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((slot * kKBlockBytes) >> 4) + (uint64_t)ks * 2);
+            tc_commit(bar(kKEmpty + slot));
           }
+          __syncwarp();
         }
-        if (*abort) {
-          give_up();
-          volatile int never = 0;  // tensor-core work ends before TMEM is released
+        if (!ok || !(ok = wait(kQFull, item & 1))) break;
+        ++item;
+        for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
+          const int sb = g & 1;
+          if (g >= 2 && !(ok = wait(kSEmpty + sb, ((g - 2) >> 1) & 1))) break;
+          const uint32_t d = tmem + kTmemS + 128 * sb;
+#pragma unroll 1
+          for (int kb = 0; kb < kKB; ++kb, ++ring) {
+            const uint32_t slot = ring % kKSlots;
+            if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
+            const uint64_t bs = kb0 + (uint64_t)((slot * kKBlockBytes) >> 4);
+            if (kb < kKB - 1) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bs + (uint64_t)ks * 2, kIdescQK, 1u);
+            }
+            if (on) tc_commit(bar(kKEmpty + slot));
+          }
+          if (ok && on) tc_commit(bar(kSFull + sb));
+        }
+        if (ok && on) tc_commit(bar(kQFree));
+      }
+      if (*abort) {
+        give_up();
+        volatile int never = 0;  // tensor-core work ends before TMEM is released
+        if (on) {
           tc_commit(bar(kDrain));
           mbar_wait(bar(kDrain), 0, &never, 10000000ull);
         }
@@ -437,35 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
       const int h = (warp & 3) * 32 + lane, half = warp >> 2;
       const bool dead = (warp & 3) * 32 >= p.H;  // a warp without heads only keeps step
-      uint32_t g = 0, item = 0;
+      uint32_t g = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
-        if (wk.lo >= wk.hi) continue;
-        ++item;
-        {  // the query: every product with the one before is complete (its S was read)
-          if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(bar(kQFull), kKBlockBytes);
-            tma_load_2d(sbase + kQ8Off, &tm_q, 8 * 64, wk.row * p.H, bar(kQFull));
-          }
-          const bool live = h < p.H;
-          const uint4* qrow = reinterpret_cast<const uint4*>(p.q + ((int64_t)wk.row * p.H + (live ? h : 0)) * kDQK) + 32 * half;
-#pragma unroll 2
-          for (int kb = 0; kb < 4; ++kb) {
-            uint32_t w[32];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const uint4 v = live ? __ldg(qrow + 8 * kb + u) : make_uint4(0u, 0u, 0u, 0u);
-              w[4 * u] = v.x;
-              w[4 * u + 1] = v.y;
-              w[4 * u + 2] = v.z;
-              w[4 * u + 3] = v.w;
-            }
-            tmem_st32(lane_addr + 32 * (4 * half + kb), w);
-          }
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(kQFull));
-        }
         float m_run = -INFINITY, l_run = 0.f;
         for (int i = wk.lo; i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
@@ -558,11 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive(bar(kStaged + stg));
         }
       }
-      if (*abort) {
-        give_up();
-        volatile int never = 0;  // block 8 of the query must land before the CTA exits
-        if (threadIdx.x == 0 && item > 0) mbar_wait(bar(kQFull), (item - 1) & 1, &never, 10000000ull);
-      }
+      if (*abort) give_up();
     }
   } else {
     // ================================================================ PV side
@@ -606,47 +615,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_wait(bar(kVFull + k % kVSlots), (k / kVSlots) & 1, &never, 10000000ull);
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        // ---- O[:, 256 n ..] += P(j) . V(j)[:, 256 n ..]
-        const uint64_t pa0 = smem_desc(sbase + kPOff, 128, 1024, kSwizzleNone);
-        const uint64_t vb0 = smem_desc(sbase, kVBlockBytes, 1024, kSwizzle128B);
-        uint32_t j = 0, ring = 0;
-        bool ok = true;
-        while (ok && wk.next(p)) {
-          for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
-            const uint32_t pb = j % kPBufs;
-            if (!(ok = mbar_wait(bar(kReady + pb), (j / kPBufs) & 1, abort, p.wait_limit_ns))) break;
-            tc_fence_after();
-            const uint64_t ad = pa0 + (uint64_t)((pb * kMsgBytes) >> 4);
+      // ---- O[:, 256 n ..] += P(j) . V(j)[:, 256 n ..]
+      const uint32_t on = elect_one();
+      const uint64_t pa0 = smem_desc(sbase + kPOff, 128, 1024, kSwizzleNone);
+      const uint64_t vb0 = smem_desc(sbase, kVBlockBytes, 1024, kSwizzle128B);
+      auto wait = [&](int which, uint32_t parity) {
+        const bool there = __all_sync(0xffffffffu, mbar_wait(bar(which), parity, abort, p.wait_limit_ns));
+        tc_fence_after();
+        return there;
+      };
+      uint32_t j = 0, ring = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
+          const uint32_t pb = j % kPBufs;
+          if (!(ok = wait(kReady + pb, (j / kPBufs) & 1))) break;
+          const uint64_t ad = pa0 + (uint64_t)((pb * kMsgBytes) >> 4);
 #pragma unroll 1
-            for (int n = 0; n < 2; ++n, ++ring) {
-              const uint32_t slot = ring % kVSlots;
-              if (!(ok = mbar_wait(bar(kVFull + slot), (ring / kVSlots) & 1, abort, p.wait_limit_ns))) break;
-              tc_fence_after();
-              const uint64_t bd = vb0 + (uint64_t)((slot * kVSlotBytes) >> 4);
+          for (int n = 0; n < 2; ++n, ++ring) {
+            const uint32_t slot = ring % kVSlots;
+            if (!(ok = wait(kVFull + slot, (ring / kVSlots) & 1))) break;
+            const uint64_t bd = vb0 + (uint64_t)((slot * kVSlotBytes) >> 4);
 #pragma unroll
-              for (int s = 0; s < kSub / 16; ++s)
-                mma_f16_ss(tmem + 256 * n, ad + (uint64_t)((s * 256) >> 4), bd + (uint64_t)((s * 2048) >> 4), kIdescPV,
-                           (i > 2 * wk.lo || s > 0) ? 1u : 0u);
-              tc_commit(bar(kVEmpty + slot));
-            }
-            if (!ok) break;
-            tc_commit_mc(bar(kPvDone + pb), 0x3);
+            for (int s = 0; s < kSub / 16; ++s)
+              mma_f16_ss_if(on, tmem + 256 * n, ad + (uint64_t)((s * 256) >> 4), bd + (uint64_t)((s * 2048) >> 4), kIdescPV,
+                            (i > 2 * wk.lo || s > 0) ? 1u : 0u);
+            if (on) tc_commit(bar(kVEmpty + slot));
           }
+          if (ok && on) tc_commit_mc(bar(kPvDone + pb), 0x3);
         }
-        if (*abort) {
-          give_up();
-          volatile int never = 0;
+      }
+      if (*abort) {
+        give_up();
+        volatile int never = 0;
+        if (on) {
           tc_commit(bar(kDrain));
           mbar_wait(bar(kDrain), 0, &never, 10000000ull);
         }
       }
-    } else if (warp < 4) {
-      // ---- rescale and epilogue: thread h owns O row h (TMEM lane h)
-      const int h = threadIdx.x;
-      const bool dead = warp * 32 >= p.H;
+    } else if (warp < 8) {
+      // ---- rescale and epilogue: thread = (head h, half of the columns)
+      const int h = (warp & 3) * 32 + lane, col0 = 256 * (warp >> 2);
+      const bool dead = (warp & 3) * 32 >= p.H;
       const uint32_t rem_stage_free = mapa_shared(bar(kStageFree), 0);
-      uint8_t* const ostage = smem + kOutOff + warp * 2048;
+      uint8_t* const ostage = smem + kOutOff + warp * 1024;
       uint32_t j = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
@@ -667,13 +679,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int cb = 0; cb < kDV / 32; ++cb) {
+              for (int c0 = col0; c0 < col0 + 256; c0 += 32) {
                 uint32_t ov[32];
-                tmem_ld32(lane_addr + 32 * cb, ov);
+                tmem_ld32(lane_addr + c0, ov);
                 tc_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
-                tmem_st32(lane_addr + 32 * cb, ov);
+                tmem_st32(lane_addr + c0, ov);
               }
               tc_wait_st();
             }
@@ -688,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ok = ok && mbar_wait(bar(kVFull + slot), (k / kVSlots) & 1, abort, p.wait_limit_ns);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              for (int e = threadIdx.x; e < (z1 - z0) * 32; e += 128) {  // 4 blocks x 8 pieces of 16 bytes per slot
+              for (int e = threadIdx.x; e < (z1 - z0) * 32; e += 256) {  // 4 blocks x 8 pieces of 16 bytes per slot
                 const int z = z0 + (e >> 5), blk = (e >> 3) & 3, c = e & 7;
                 *reinterpret_cast<uint4*>(smem + slot * kVSlotBytes + blk * kVBlockBytes + z * 128 + c * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
@@ -699,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(bar(kReady + pb));
-          if (h == 0) mbar_arrive_cluster(rem_stage_free + 8u * (j % kStages));
+          if (threadIdx.x == 0) mbar_arrive_cluster(rem_stage_free + 8u * (j % kStages));
         }
         if (!ok) break;
         const bool any = wk.lo < wk.hi;
@@ -712,29 +724,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool whole = wk.hi - wk.lo == wk.chunks;
         const float mul = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
         const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
-        const bool as_bf16 = whole && p.out_bf16;
-        // 64 bytes of 32 rows at a time through shared memory, so that four
-        // lanes write a row's piece
-        uint8_t* const rowp = ostage + lane * 64;
-        const int sw = (lane >> 1) & 3;
-        const int64_t row_bytes = as_bf16 ? kDV * 2 : kDV * 4;
-        uint8_t* const gout = whole ? reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.row * p.H + warp * 32) * row_bytes
-                                    : reinterpret_cast<uint8_t*>(p.part_o) + (part * p.H + warp * 32) * row_bytes;
-        auto flush = [&](int64_t col_byte) {
+        // Partials: [column / 4][head][4], so that a warp's stores are whole
+        // lines.  Finished rows: 32 bytes of 32 rows at a time through shared
+        // memory, so that two lanes write a row's piece.
+        float4* const pout = reinterpret_cast<float4*>(p.part_o + part * p.H * kDV) + h;
+        uint8_t* const rowp = ostage + lane * 32;
+        const int sw = (lane >> 2) & 1;
+        const int elt = p.out_bf16 ? 2 : 4;
+        uint8_t* const gout =
+            reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.row * p.H + (warp & 3) * 32) * (int64_t)(kDV * elt);
+        auto flush = [&](int col_byte) {
           __syncwarp();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int rr = 8 * u + (lane >> 2), c = lane & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-            if (warp * 32 + rr < p.H) *reinterpret_cast<uint4*>(gout + rr * row_bytes + col_byte + 16 * c) = v;
+          for (int u = 0; u < 2; ++u) {
+            const int rr = 16 * u + (lane >> 1), c = lane & 1;
+            const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 32 + ((c ^ ((rr >> 2) & 1)) << 4));
+            if ((warp & 3) * 32 + rr < p.H)
+              *reinterpret_cast<uint4*>(gout + rr * (kDV * elt) + col_byte + 16 * c) = v;
           }
           __syncwarp();
         };
 #pragma unroll 1
-        for (int cb = 0; cb < kDV / 32; ++cb) {
+        for (int c0 = col0; c0 < col0 + 256; c0 += 32) {
           uint32_t ov[32];
           if (any) {
-            tmem_ld32(lane_addr + 32 * cb, ov);
+            tmem_ld32(lane_addr + c0, ov);
             tc_wait_ld();
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = l == 0.f && whole ? 0u : __float_as_uint(__uint_as_float(ov[c]) * mul);
@@ -742,37 +756,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
           }
-          if (as_bf16) {
+          if (!whole) {
+            if (h < p.H) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 t2 =
-                    __floats2bfloat162_rn(__uint_as_float(ov[8 * c + 2 * e]), __uint_as_float(ov[8 * c + 2 * e + 1]));
-                w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
-              }
-              *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              for (int c = 0; c < 8; ++c)
+                pout[(int64_t)(c0 / 4 + c) * p.H] =
+                    make_float4(__uint_as_float(ov[4 * c]), __uint_as_float(ov[4 * c + 1]), __uint_as_float(ov[4 * c + 2]),
+                                __uint_as_float(ov[4 * c + 3]));
             }
-            flush(cb * 64);
-          } else {
+          } else if (p.out_bf16) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 2; ++c) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 t2 = __floats2bfloat162_rn(__uint_as_float(ov[16 * hf + 8 * c + 2 * e]),
+                                                                   __uint_as_float(ov[16 * hf + 8 * c + 2 * e + 1]));
+                  w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+                }
+                *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
+              flush(c0 * 2 + hf * 32);
+            }
+          } else {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
                 *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) =
-                    make_uint4(ov[16 * hf + 4 * c], ov[16 * hf + 4 * c + 1], ov[16 * hf + 4 * c + 2], ov[16 * hf + 4 * c + 3]);
-              flush(cb * 128 + hf * 64);
+                    make_uint4(ov[8 * q4 + 4 * c], ov[8 * q4 + 4 * c + 1], ov[8 * q4 + 4 * c + 2], ov[8 * q4 + 4 * c + 3]);
+              flush(c0 * 4 + q4 * 32);
             }
           }
         }
         tc_fence_before();  // O is read: the next row's first product (after Ready) may overwrite it
-        if (h < p.H) {
+        if (h < p.H && col0 == 0) {
           if (whole) {
             if (p.lse) p.lse[(int64_t)wk.row * p.H + h] = l == 0.f ? -INFINITY : (m_row + log2f(l)) * 0.69314718055994531f;
           } else {
-            p.part_ml[2 * (part * p.H + h)] = m_row;
-            p.part_ml[2 * (part * p.H + h) + 1] = l;
+            p.part_ml[2 * part * p.H + h] = m_row;
+            p.part_ml[(2 * part + 1) * p.H + h] = l;
           }
         }
       }
@@ -792,17 +817,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of the cut rows: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// One CTA per (cut row, head), in turn; thread = (four columns, half of the partials).
-constexpr int kCombineThreads = 256;
+// A task is (cut row, 32 heads, 8 / SPLIT column quads); lane = head, and SPLIT
+// warps share a row's partials, their sums meeting in shared memory in a
+// fixed order.
+constexpr int kCombineWarps = 8;
 constexpr int kMaxClusters = 128;
 
-__global__ void __launch_bounds__(kCombineThreads)
+template <int SPLIT>
+__global__ void __launch_bounds__(32 * kCombineWarps)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
-                             const float* __restrict__ part_o, int n_clusters, int H, void* out, int out_bf16, float* lse) {
+                             const float4* __restrict__ part_o, int n_clusters, int H, void* out, int out_bf16, float* lse) {
+  constexpr int kQuads = kCombineWarps / SPLIT;  // column quads per task
   __shared__ CutRow s_cut[kMaxClusters];
   __shared__ int s_n;
-  __shared__ float s_w[kMaxClusters], s_ml[2];
-  __shared__ float4 s_half[128];
+  __shared__ float s_sum[kCombineWarps][5][32];
   grid_dependency_wait();
   allow_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -818,63 +846,61 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int tasks = s_n * H;
+  const int hgroups = (H + 31) / 32, per_row = hgroups * (kDV / 4 / kQuads);
+  const int tasks = s_n * per_row;
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const CutRow c = s_cut[task / H];
-    const int h = task % H;
+    const CutRow c = s_cut[task / per_row];
+    const int rest = task % per_row;
+    const int h = rest % hgroups * 32 + lane, quad = rest / hgroups * kQuads + warp / SPLIT, sub = warp % SPLIT;
     // the first partial is its cluster's second, the others are their clusters' first
-    auto part = [&](int i) -> int64_t { return ((int64_t)2 * (c.first + i) + (i == 0 ? 1 : 0)) * H + h; };
-    if (warp == 0) {
-      float M = -INFINITY;
-      for (int i = lane; i < c.count; i += 32) M = fmaxf(M, part_ml[2 * part(i)]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float sub = M == -INFINITY ? 0.f : M;
-      float l = 0.f;
-      for (int i = lane; i < c.count; i += 32) {
-        const float w = exp2f(part_ml[2 * part(i)] - sub);
-        s_w[i] = w;
-        l += w * part_ml[2 * part(i) + 1];
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        s_ml[0] = M;
-        s_ml[1] = l;
-      }
-    }
-    __syncthreads();
-    const int c4 = threadIdx.x & 127, hf = threadIdx.x >> 7;
+    auto part = [&](int i) -> int64_t { return 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0); };
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, l = 0.f;
+    if (h < H) {
 #pragma unroll 8
-    for (int i = hf; i < c.count; i += 2) {
-      const float w = s_w[i];
-      const float4 o = __ldg(reinterpret_cast<const float4*>(part_o + part(i) * kDV) + c4);
-      if (w != 0.f) {  // a partial without any visible slot holds nothing
+      for (int i = 0; i < c.count; ++i) M = fmaxf(M, __ldg(part_ml + 2 * part(i) * H + h));
+      const float off = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+      for (int i = sub; i < c.count; i += SPLIT) {
+        const float4 o = __ldg(part_o + (part(i) * (kDV / 4) + quad) * H + h);
+        const float w = exp2f(__ldg(part_ml + 2 * part(i) * H + h) - off);
+        l = fmaf(w, __ldg(part_ml + (2 * part(i) + 1) * H + h), l);
         a.x = fmaf(w, o.x, a.x);
         a.y = fmaf(w, o.y, a.y);
         a.z = fmaf(w, o.z, a.z);
         a.w = fmaf(w, o.w, a.w);
       }
     }
-    if (hf == 1) s_half[c4] = a;
-    __syncthreads();
-    if (hf == 0) {
-      const float4 o = s_half[c4];
-      const float l = s_ml[1], inv = l == 0.f ? 0.f : 1.f / l;
-      a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                   : make_float4((a.x + o.x) * inv, (a.y + o.y) * inv, (a.z + o.z) * inv, (a.w + o.w) * inv);
-      const int64_t rh = (int64_t)c.row * H + h;
-      if (out_bf16) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
-        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[c4] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-      } else {
-        reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + rh * kDV)[c4] = a;
+    if (SPLIT > 1) {
+      __syncthreads();  // the sums of the task before are read
+      s_sum[warp][0][lane] = a.x;
+      s_sum[warp][1][lane] = a.y;
+      s_sum[warp][2][lane] = a.z;
+      s_sum[warp][3][lane] = a.w;
+      s_sum[warp][4][lane] = l;
+      __syncthreads();
+      if (sub != 0) continue;
+#pragma unroll
+      for (int u = 1; u < SPLIT; ++u) {
+        a.x += s_sum[warp + u][0][lane];
+        a.y += s_sum[warp + u][1][lane];
+        a.z += s_sum[warp + u][2][lane];
+        a.w += s_sum[warp + u][3][lane];
+        l += s_sum[warp + u][4][lane];
       }
-      if (c4 == 0 && lse) lse[rh] = l == 0.f ? -INFINITY : (s_ml[0] + log2f(l)) * 0.69314718055994531f;
     }
-    __syncthreads();
+    if (h >= H) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    const int64_t rh = (int64_t)c.row * H + h;
+    if (out_bf16) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
+      reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[quad] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    } else {
+      reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + rh * kDV)[quad] = a;
+    }
+    if (quad == 0 && lse) lse[rh] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -967,10 +993,16 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tkv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
-  const unsigned grid = (unsigned)std::min<int64_t>((int64_t)(n - 1) * H, 8 * (int64_t)device_info().sm_count);
-  if (n > 1 && launch_pdl(paged_mla_combine_kernel, dim3(grid), dim3(kCombineThreads), 0, s, (const CutRow*)p.cut,
-                          (const float*)p.part_ml, (const float*)p.part_o, n, H, out, p.out_bf16, lse) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  if (n > 1) {
+    // a few rows are cut into many partials, many rows into two or three
+    const bool few = p.n_rows <= 4;
+    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * ((H + 31) / 32) * (kDV / 4) * (few ? 4 : 1) / kCombineWarps;
+    const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * kCombineWarps);
+    const auto kernel = few ? paged_mla_combine_kernel<4> : paged_mla_combine_kernel<1>;
+    if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml,
+                   reinterpret_cast<const float4*>(p.part_o), n, H, out, p.out_bf16, lse) != cudaSuccess)
+      return DSA_ERR_CUDA;
+  }
   return DSA_OK;
 }
 
