@@ -23,8 +23,8 @@
 //     ring of eight; S = Q.K^T (N = 128) goes to one of two TMEM buffers.
 //     Eight softmax warps, thread = (head, half of the chunk's slots); the
 //     halves' maxima meet in shared memory, P is rounded to bf16 (the tensor
-//     core's operand; its sum l is kept unrounded in fp32) and sent to CTA 1
-//     by the copy engine, 64 slots at a time, with the rescale factor.
+//     core's operand; its sum l is kept unrounded in fp32) and two warps store
+//     it into CTA 1's shared memory, 64 slots at a time, with the rescale factor.
 //   CTA 1 (PV side): O in TMEM.  The rows' first 512 columns arrive by TMA as
 //     64-slot x 256-column tiles in a ring of five (they come out of L2, where
 //     CTA 0's loads have put them); O += P.V in two N = 256 halves per 64
@@ -49,27 +49,30 @@ namespace {
 constexpr int kChunk = 128;              // slots per chunk: the QK product's N
 constexpr int kSub = 64;                 // slots per message to CTA 1
 constexpr int kKB = kDQK / 64;           // 64-column blocks of a row: 9
-constexpr int kKBlockBytes = kChunk * 128;
+constexpr int kQBlockBytes = 128 * 128;             // a 64-column block of the query, 128 heads
+constexpr int kVBlockBytes = kSub * 128;            // a 64-column block of 64 rows
 constexpr int kRowUnits = 2;             // what a row costs besides its chunks, in chunks
 
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10;
 constexpr int kSoftmaxThreads = 256;
+constexpr int kSendThreads = kThreads - 32 * kSendWarp;
 
 constexpr int kPBytes = 128 * kSub * 2;             // P: 128 heads x 64 slots, bf16
 constexpr uint32_t kMsgBytes = kPBytes + 3 * 512;   // then alpha, l, m per head
 // ---- CTA 0 shared memory
 constexpr int kQ8Off = 0;
-constexpr int kKSlots = 8;
-constexpr int kKRingOff = kKBlockBytes;
-constexpr int kStages = 4;
-constexpr int kStageOff = kKRingOff + kKSlots * kKBlockBytes;     // 147456
-constexpr int kMaxOff = kStageOff + kStages * (int)kMsgBytes;     // 219136: maxima [2][2][128]
+constexpr int kKSlotBlocks = 3;                     // a ring slot: 64 slots x three 64-column blocks
+constexpr int kKSlotBytes = kKSlotBlocks * kVBlockBytes;
+constexpr int kKSlots = 6;
+constexpr int kKRingOff = kQBlockBytes;
+constexpr int kStages = 3;
+constexpr int kStageOff = kKRingOff + kKSlots * kKSlotBytes;      // 163840
+constexpr int kMaxOff = kStageOff + kStages * (int)kMsgBytes;     // 217600: maxima [2][2][128]
 constexpr int kMaskOff = kMaxOff + 2 * 2 * 128 * 4;               // validity words [4][4]
 constexpr int kQkEnd = kMaskOff + 4 * 16;
 // ---- CTA 1 shared memory
 constexpr int kVSlotBytes = kSub * 512;             // 64 slots x 256 columns
-constexpr int kVBlockBytes = kSub * 128;            // 64 slots x 64 columns
 constexpr int kVSlots = 5;
 constexpr int kPBufs = 3;
 constexpr int kPOff = kVSlots * kVSlotBytes;                      // 163840
@@ -80,13 +83,13 @@ constexpr int kBarOff = (kQkEnd > kPvEnd ? kQkEnd : kPvEnd);
 enum Bar : int {
   kQFull = 0,                       // CTA 0: query block 8 has landed
   kQFree,                           // CTA 0: the products of a part are complete
-  kKFull,                           // [8] CTA 0
-  kKEmpty = kKFull + kKSlots,       // [8] CTA 0
+  kKFull,                           // [6] CTA 0
+  kKEmpty = kKFull + kKSlots,       // [6] CTA 0
   kSFull = kKEmpty + kKSlots,       // [2] CTA 0
   kSEmpty = kSFull + 2,             // [2] CTA 0
   kMaskFull = kSEmpty + 2,          // [4] CTA 0: the chunk's validity words are written
-  kStaged = kMaskFull + 4,          // [4] CTA 0: a message is staged
-  kStageFree = kStaged + kStages,   // [4] CTA 0: its copy has landed in CTA 1
+  kStaged = kMaskFull + 4,          // [3] CTA 0: a message is staged
+  kStageFree = kStaged + kStages,   // [3] CTA 0: it is read
   kPvDone = kStageFree + kStages,   // [3] both: the product of a message is complete
   kVFull = kPvDone + kPBufs,        // [5] CTA 1
   kVEmpty = kVFull + kVSlots,       // [5] CTA 1
@@ -106,7 +109,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBarOff % 8 == 0 && kMiscOff % 8 == 0 && kMsgBytes % 16 == 0 && kStageOff % 128 == 0 && kPOff % 128 == 0, "alignment");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // CTA 0: query blocks 0-7 in [0, 256), S buffers at 256 and 384
-constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk);
+constexpr uint32_t kIdescQK = idesc_bf16(128, kSub);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
 
 // A row that part boundaries cut, as the combine kernel sees it.
@@ -118,7 +121,6 @@ struct CutRow {
 };
 
 struct PagedMlaParams {
-  const __nv_bfloat16* q;
   PagePool pool;
   const int32_t* lens;
   int n_rows, T, H, n_clusters;
@@ -172,8 +174,8 @@ struct Walk {
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                     const PagedMlaParams p) {
+    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const PagedMlaParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -192,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) misc->abort = 0;
   if (warp == kMmaWarp) {
     if (lane == 0) {
-      tma_prefetch_desc(&tm_kv);
+      tma_prefetch_desc(rank == 0 ? &tm_k : &tm_v);
       mbar_init(bar(kQFull), 1 + p.debug_stall);
       mbar_init(bar(kQFree), 1);
       for (int i = 0; i < kKSlots; ++i) {
@@ -201,17 +203,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(kSFull + i), 1);
-        mbar_init(bar(kSEmpty + i), kSoftmaxThreads);
+        mbar_init(bar(kSEmpty + i), kSoftmaxThreads / 32);
       }
       for (int i = 0; i < 4; ++i) mbar_init(bar(kMaskFull + i), 1);
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(bar(kStaged + i), 128);
-        mbar_init(bar(kStageFree + i), 1);
+        mbar_init(bar(kStaged + i), 4);
+        mbar_init(bar(kStageFree + i), kSendThreads / 32);
       }
       for (int i = 0; i < kPBufs; ++i) {
         mbar_init(bar(kPvDone + i), 1);
         mbar_init(bar(kPFull + i), 1);
-        mbar_init(bar(kReady + i), 256);
+        mbar_init(bar(kReady + i), 8);
       }
       for (int i = 0; i < kVSlots; ++i) {
         mbar_init(bar(kVFull + i), 1);
@@ -308,7 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (rank == 0) {
     // ================================================================ QK side
     if (warp == kLoadWarp) {
-      // ---- the chunks' blocks: lane i < 2 * nbox64 loads box i of a block
+      // ---- the chunks' blocks: lane i < 2 * nbox64 locates box i
+      const uint32_t on = elect_one();
       uint32_t g = 0, ring = 0, item = 0;  // chunk, block and part counters
       bool ok = true;
       while (ok && wk.next(p)) {
@@ -338,16 +341,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int kb = 0; kb < kKB - 1; ++kb, ++ring) {
           const uint32_t slot = ring % kKSlots;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(kKFull + slot), kKBlockBytes);
-            tma_load_2d(sbase + kKRingOff + slot * kKBlockBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + slot));
+          if (!(ok = warp_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
+          if (on) {
+            mbar_arrive_expect_tx(bar(kKFull + slot), kQBlockBytes);
+            tma_load_2d(sbase + kKRingOff + slot * kKSlotBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + slot));
           }
         }
         if (!ok) break;
-        if (item > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns)))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kQFull), kKBlockBytes);
+        if (item > 0 && !(ok = warp_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns))) break;
+        if (on) {
+          mbar_arrive_expect_tx(bar(kQFull), kQBlockBytes);
           tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.row * p.H, bar(kQFull));
         }
         ++item;
@@ -364,14 +367,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
           if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
+          int32_t yb[8];
+#pragma unroll
+          for (int bx = 0; bx < 8; ++bx) yb[bx] = __shfl_sync(0xffffffffu, y, bx);
 #pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb, ++ring) {
+          for (int part = 0; part < 2 * (kKB / kKSlotBlocks); ++part, ++ring) {
             const uint32_t slot = ring % kKSlots;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + slot), kKBlockBytes);
+            if (!(ok = warp_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
+            const bool second = part >= kKB / kKSlotBlocks;
+            const int kb = kKSlotBlocks * (second ? part - kKB / kKSlotBlocks : part);
+            if (on) {
+              const uint32_t dst = sbase + kKRingOff + slot * kKSlotBytes, full = bar(kKFull + slot);
+              mbar_arrive_expect_tx(full, kKSlotBytes);
+              if (p.box == 64) {
+                tma_load_3d(dst, &tm_k, 0, second ? yb[1] : yb[0], kb, full);
+              } else if (p.box == 32) {
+#pragma unroll
+                for (int bx = 0; bx < 2; ++bx)
+#pragma unroll
+                  for (int blk = 0; blk < kKSlotBlocks; ++blk)
+                    tma_load_2d(dst + blk * kVBlockBytes + bx * 32 * 128, &tm_k, (kb + blk) * 64, second ? yb[2 + bx] : yb[bx], full);
+              } else {
+#pragma unroll
+                for (int bx = 0; bx < 4; ++bx)
+#pragma unroll
+                  for (int blk = 0; blk < kKSlotBlocks; ++blk)
+                    tma_load_2d(dst + blk * kVBlockBytes + bx * 16 * 128, &tm_k, (kb + blk) * 64, second ? yb[4 + bx] : yb[bx], full);
+              }
+            }
             __syncwarp();
-            if (lane < nbox)
-              tma_load_2d(sbase + kKRingOff + slot * kKBlockBytes + lane * p.box * 128, &tm_kv, kb * 64, y, bar(kKFull + slot));
           }
           y = y_next;
           valid = valid_next;
@@ -390,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t q8 = smem_desc(sbase + kQ8Off, 16, 1024, kSwizzle128B);
       const uint64_t kb0 = smem_desc(sbase + kKRingOff, 16, 1024, kSwizzle128B);
       auto wait = [&](int which, uint32_t parity) {
-        const bool there = __all_sync(0xffffffffu, mbar_wait(bar(which), parity, abort, p.wait_limit_ns));
+        const bool there = warp_wait(bar(which), parity, abort, p.wait_limit_ns);
         tc_fence_after();
         return there;
       };
@@ -407,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (on) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((slot * kKBlockBytes) >> 4) + (uint64_t)ks * 2);
+              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((slot * kKSlotBytes) >> 4) + (uint64_t)ks * 2);
             tc_commit(bar(kKEmpty + slot));
           }
           __syncwarp();
@@ -417,21 +441,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(kSEmpty + sb, ((g - 2) >> 1) & 1))) break;
-          const uint32_t d = tmem + kTmemS + 128 * sb;
-#pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb, ++ring) {
-            const uint32_t slot = ring % kKSlots;
-            if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
-            const uint64_t bs = kb0 + (uint64_t)((slot * kKBlockBytes) >> 4);
-            if (kb < kKB - 1) {
+          for (int half = 0; ok && half < 2; ++half) {
+            const uint32_t d = tmem + kTmemS + 128 * sb + 64 * half;
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
-            } else {
+            for (int part = 0; part < kKB / kKSlotBlocks; ++part, ++ring) {
+              const uint32_t slot = ring % kKSlots;
+              if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
+              const uint64_t bs = kb0 + (uint64_t)((slot * kKSlotBytes) >> 4);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bs + (uint64_t)ks * 2, kIdescQK, 1u);
+              for (int blk = 0; blk < kKSlotBlocks; ++blk) {
+                const int kb = kKSlotBlocks * part + blk;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                  const uint64_t bd = bs + (uint64_t)((blk * kVBlockBytes) >> 4) + (uint64_t)ks * 2;
+                  if (kb < kKB - 1) mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bd, kIdescQK, (kb | ks) ? 1u : 0u);
+                  else mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bd, kIdescQK, 1u);
+                }
+              }
+              if (on) tc_commit(bar(kKEmpty + slot));
             }
-            if (on) tc_commit(bar(kKEmpty + slot));
           }
           if (ok && on) tc_commit(bar(kSFull + sb));
         }
@@ -445,33 +473,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_wait(bar(kDrain), 0, &never, 10000000ull);
         }
       }
-    } else if (warp == kSendWarp) {
-      if (lane == 0) {
-        // ---- message j (64 slots of P, alpha, l, m) to CTA 1's buffer j % 3
-        const uint32_t rem_msg = mapa_shared(sbase + kPOff, 1);
-        const uint32_t rem_pfull = mapa_shared(bar(kPFull), 1);
-        uint32_t j = 0;
-        bool ok = true;
-        while (ok && wk.next(p)) {
-          for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
-            const uint32_t st = j % kStages, pb = j % kPBufs;
-            if (!(ok = mbar_wait(bar(kStaged + st), (j / kStages) & 1, abort, p.wait_limit_ns))) break;
-            if (j >= kPBufs &&
-                !(ok = mbar_wait_cluster(bar(kPvDone + pb), ((j / kPBufs) - 1) & 1, abort, p.wait_limit_ns))) break;
-            mbar_arrive_expect_tx_cluster(rem_pfull + 8u * pb, kMsgBytes);
-            bulk_copy_s2c(rem_msg + pb * kMsgBytes, sbase + kStageOff + st * kMsgBytes, kMsgBytes, rem_pfull + 8u * pb);
+    } else if (warp >= kSendWarp) {
+      // ---- message j (64 slots of P, alpha, l, m) to CTA 1's buffer j % 3:
+      // two warps read the staged message and store it into the partner's
+      // shared memory.  (The copy engine would take it too, but behind the
+      // block loads in its queue: 2600 cycles a message against 970 without.)
+      const uint32_t rem_msg = mapa_shared(sbase + kPOff, 1);
+      const uint32_t rem_pfull = mapa_shared(bar(kPFull), 1);
+      const int tid = threadIdx.x - kSendWarp * 32;
+      constexpr int kPieces = (int)kMsgBytes / 16, kBatch = 9;
+      static_assert(kPieces <= 2 * kBatch * kSendThreads, "two rounds per message");
+      uint32_t j = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
+          const uint32_t st = j % kStages, pb = j % kPBufs;
+          ok = warp_wait(bar(kStaged + st), (j / kStages) & 1, abort, p.wait_limit_ns) &&
+               (j < kPBufs || warp_wait<true>(bar(kPvDone + pb), ((j / kPBufs) - 1) & 1, abort, p.wait_limit_ns));
+          if (!ok) break;
+          const uint32_t full = rem_pfull + 8u * pb, dst = rem_msg + pb * kMsgBytes;
+          const uint8_t* const src = smem + kStageOff + st * kMsgBytes;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int e = (r * kBatch + k) * kSendThreads + tid;
+              if (e < kPieces) v[k] = *reinterpret_cast<const uint4*>(src + 16 * e);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int e = (r * kBatch + k) * kSendThreads + tid;
+              if (e < kPieces) st_async_v4(dst + 16 * e, v[k], full);
+            }
           }
-        }
-        // CTA 1's last arrivals here must land before this CTA exits
-        for (uint32_t k = j > kPBufs ? j - kPBufs : 0; ok && k < j; ++k)
-          ok = mbar_wait_cluster(bar(kPvDone + k % kPBufs), (k / kPBufs) & 1, abort, p.wait_limit_ns);
-        if (*abort) {
-          give_up();
-          volatile int never = 0;  // the copies must have left the staging buffers
-          for (uint32_t k = j > kStages ? j - kStages : 0; k < j; ++k)
-            mbar_wait_cluster(bar(kStageFree + k % kStages), (k / kStages) & 1, &never, 10000000ull);
+          warp_arrive(bar(kStageFree + st));  // the message is read
         }
       }
+      // CTA 1's last arrivals here must land before this CTA exits
+      for (uint32_t k = j > kPBufs ? j - kPBufs : 0; ok && k < j; ++k)
+        ok = warp_wait<true>(bar(kPvDone + k % kPBufs), (k / kPBufs) & 1, abort, p.wait_limit_ns);
+      if (*abort) give_up();
     } else if (warp < 8) {
       // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
       const int h = (warp & 3) * 32 + lane, half = warp >> 2;
@@ -483,9 +525,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = wk.lo; i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
           const uint32_t j = 2 * g + half, stg = j % kStages;
-          ok = mbar_wait(bar(kMaskFull + (g & 3)), (g >> 2) & 1, abort, p.wait_limit_ns) &&
-               mbar_wait(bar(kSFull + sb), (g >> 1) & 1, abort, p.wait_limit_ns);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = warp_wait(bar(kMaskFull + (g & 3)), (g >> 2) & 1, abort, p.wait_limit_ns) &&
+               warp_wait(bar(kSFull + sb), (g >> 1) & 1, abort, p.wait_limit_ns);
           uint32_t sv[64];
           float mx = -INFINITY;
           if (ok) {
@@ -497,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_before();
             const uint32_t* vm = reinterpret_cast<const uint32_t*>(smem + kMaskOff) + 4 * (g & 3) + 2 * half;
             const uint32_t vm0 = vm[0], vm1 = vm[1];
-            mbar_arrive(bar(kSEmpty + sb));
+            warp_arrive(bar(kSEmpty + sb));
             if (!dead) {
               // x = s * scale * log2(e); masked slots -inf
 #pragma unroll
@@ -524,8 +565,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
               reinterpret_cast<float*>(smem + kMaxOff)[256 * sb + 128 * half + h] = mx;
             }
-            // the staging buffer is free once the copy of message j - 4 has landed
-            if (g >= 2) ok = mbar_wait_cluster(bar(kStageFree + stg), ((j / kStages) - 1) & 1, abort, p.wait_limit_ns);
+            // the staging buffer is free once message j - 3 is read
+            if (j >= kStages) ok = warp_wait(bar(kStageFree + stg), ((j / kStages) - 1) & 1, abort, p.wait_limit_ns);
           }
           // both halves' maxima are written; all eight warps leave together
           if (named_barrier_or(1, kSoftmaxThreads, !ok)) {
@@ -567,8 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             reinterpret_cast<float*>(stage + kPBytes)[h] = 1.f;
           }
-          fence_proxy_async_smem();  // the copy engine reads the message
-          mbar_arrive(bar(kStaged + stg));
+          warp_arrive(bar(kStaged + stg));
         }
       }
       if (*abort) give_up();
@@ -576,16 +616,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     // ================================================================ PV side
     if (warp == kLoadWarp) {
-      // ---- 64-slot x 256-column tiles: lane i < 4 * nbox64 loads box
-      // i % nbox64 of column block i / nbox64
+      // ---- 64-slot x 256-column tiles: lane i < nbox64 locates box i
       uint32_t ring = 0;
       bool ok = true;
-      const int bx = lane % nbox64, blk = lane / nbox64;
+      const uint32_t on = elect_one();
       while (ok && wk.next(p)) {
         const int b = wk.row / p.T;
         auto locate = [&](int i) -> int32_t {  // i counts 64-slot halves
-          const int64_t s = (int64_t)i * kSub + bx * p.box;
-          if (blk < 4 && s < wk.len) {
+          const int64_t s = (int64_t)i * kSub + lane * p.box;
+          if (lane < nbox64 && s < wk.len) {
             const int64_t row = pool_row(p.pool, b, (int32_t)s);
             if (row >= 0) return (int32_t)row;
           }
@@ -595,15 +634,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (wk.lo < wk.hi) y = locate(2 * wk.lo);
         for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i) {
           if (i + 1 < 2 * wk.hi) y_next = locate(i + 1);
+          int32_t yb[4];
+#pragma unroll
+          for (int bx = 0; bx < 4; ++bx) yb[bx] = __shfl_sync(0xffffffffu, y, bx);
 #pragma unroll
           for (int n = 0; n < 2; ++n, ++ring) {
             const uint32_t slot = ring % kVSlots;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kVEmpty + slot), ((ring / kVSlots) & 1) ^ 1, abort, p.wait_limit_ns)))) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + slot), kVSlotBytes);
+            if (!(ok = warp_wait(bar(kVEmpty + slot), ((ring / kVSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
+            if (on) {
+              mbar_arrive_expect_tx(bar(kVFull + slot), kVSlotBytes);
+              const uint32_t dst = sbase + slot * kVSlotBytes, full = bar(kVFull + slot);
+              if (p.box == 64) {
+                tma_load_3d(dst, &tm_v, 0, yb[0], 4 * n, full);
+              } else if (p.box == 32) {
+#pragma unroll
+                for (int bx = 0; bx < 2; ++bx)
+#pragma unroll
+                  for (int blk = 0; blk < 4; ++blk)
+                    tma_load_2d(dst + blk * kVBlockBytes + bx * 32 * 128, &tm_v, 256 * n + 64 * blk, yb[bx], full);
+              } else {
+#pragma unroll
+                for (int bx = 0; bx < 4; ++bx)
+#pragma unroll
+                  for (int blk = 0; blk < 4; ++blk)
+                    tma_load_2d(dst + blk * kVBlockBytes + bx * 16 * 128, &tm_v, 256 * n + 64 * blk, yb[bx], full);
+              }
+            }
             __syncwarp();
-            if (blk < 4)
-              tma_load_2d(sbase + slot * kVSlotBytes + blk * kVBlockBytes + bx * p.box * 128, &tm_kv, 256 * n + 64 * blk, y,
-                          bar(kVFull + slot));
           }
           y = y_next;
         }
@@ -620,7 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t pa0 = smem_desc(sbase + kPOff, 128, 1024, kSwizzleNone);
       const uint64_t vb0 = smem_desc(sbase, kVBlockBytes, 1024, kSwizzle128B);
       auto wait = [&](int which, uint32_t parity) {
-        const bool there = __all_sync(0xffffffffu, mbar_wait(bar(which), parity, abort, p.wait_limit_ns));
+        const bool there = warp_wait(bar(which), parity, abort, p.wait_limit_ns);
         tc_fence_after();
         return there;
       };
@@ -653,11 +710,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_wait(bar(kDrain), 0, &never, 10000000ull);
         }
       }
+    } else if (warp == kSendWarp) {
+      // ---- expects message j in buffer j % 3 once that buffer is free.  (Done
+      // here and not by the sender: an arrival on another CTA's barrier
+      // releases the thread's earlier stores first, which took 2000 cycles.)
+      uint32_t j = 0;
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
+          const uint32_t pb = j % kPBufs;
+          ok = j < kPBufs || warp_wait(bar(kPvDone + pb), ((j / kPBufs) - 1) & 1, abort, p.wait_limit_ns);
+          if (ok && lane == 0) mbar_arrive_expect_tx(bar(kPFull + pb), kMsgBytes);
+        }
+      }
+      if (*abort) give_up();
     } else if (warp < 8) {
       // ---- rescale and epilogue: thread = (head h, half of the columns)
       const int h = (warp & 3) * 32 + lane, col0 = 256 * (warp >> 2);
       const bool dead = (warp & 3) * 32 >= p.H;
-      const uint32_t rem_stage_free = mapa_shared(bar(kStageFree), 0);
       uint8_t* const ostage = smem + kOutOff + warp * 1024;
       uint32_t j = 0;
       bool ok = true;
@@ -665,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float l_half[2] = {0.f, 0.f}, m_row = -INFINITY;
         for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
           const uint32_t pb = j % kPBufs;
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(kPFull + pb), (j / kPBufs) & 1, abort, p.wait_limit_ns));
+          ok = warp_wait<true>(bar(kPFull + pb), (j / kPBufs) & 1, abort, p.wait_limit_ns);
           if (!ok) break;
           const float* tail = reinterpret_cast<const float*>(smem + kPOff + pb * kMsgBytes + kPBytes);
           if (!dead) {
@@ -675,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m_row = tail[256 + h];
             if (i > 2 * wk.lo && __any_sync(0xffffffffu, alpha != 1.f)) {
               // every product so far is complete when the last one is
-              ok = __all_sync(0xffffffffu, mbar_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns));
+              ok = warp_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -697,8 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (uint32_t n = 0; n < 2; ++n) {
               const uint32_t k = 2 * j + n, slot = k % kVSlots;
-              ok = ok && mbar_wait(bar(kVFull + slot), (k / kVSlots) & 1, abort, p.wait_limit_ns);
-              ok = __all_sync(0xffffffffu, ok);
+              ok = warp_wait(bar(kVFull + slot), (k / kVSlots) & 1, abort, p.wait_limit_ns);
               if (!ok) break;
               for (int e = threadIdx.x; e < (z1 - z0) * 32; e += 256) {  // 4 blocks x 8 pieces of 16 bytes per slot
                 const int z = z0 + (e >> 5), blk = (e >> 3) & 3, c = e & 7;
@@ -710,13 +779,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          mbar_arrive(bar(kReady + pb));
-          if (threadIdx.x == 0) mbar_arrive_cluster(rem_stage_free + 8u * (j % kStages));
+          warp_arrive(bar(kReady + pb));
         }
         if (!ok) break;
         const bool any = wk.lo < wk.hi;
         if (any)
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns));
+          ok = warp_wait(bar(kPvDone + (j - 1) % kPBufs), ((j - 1) / kPBufs) & 1, abort, p.wait_limit_ns);
         if (!ok) break;
         if (dead) continue;
         tc_fence_after();
@@ -966,7 +1034,6 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   take_attention_debug(debug);
   const int n = paged_clusters();
   PagedMlaParams p;
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.pool = PagePool{page_table, ld_table, n_pages, max_pages, page_size};
   p.lens = lens;
   p.n_rows = B * T;
@@ -984,14 +1051,25 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
   p.wait_limit_ns = debug.wait_limit_ns;
-  CUtensorMap tq, tkv;
-  if (!make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tkv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)n_pages * page_size, kDQK * 2, 64,
-                    (uint32_t)p.box, CU_TENSOR_MAP_SWIZZLE_128B))
-    return DSA_ERR_CUDA;
+  CUtensorMap tq, tk, tv;
+  const uint64_t rows = (uint64_t)n_pages * page_size;
+  bool maps = make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+  if (p.box == 64) {
+    // a ring slot is one box: 64 rows of three (K) or four (V) column blocks
+    const uint64_t dims[3] = {64, rows, kKB}, strides[2] = {kDQK * 2, 128};
+    const uint32_t box_k[3] = {64, 64, kKSlotBlocks}, box_v[3] = {64, 64, 4};
+    maps = maps &&
+           make_tmap_3d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_k, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_tmap_3d(&tv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_v, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    maps = maps && make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, rows, kDQK * 2, 64, (uint32_t)p.box,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+    tv = tk;
+  }
+  if (!maps) return DSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tkv, p) != cudaSuccess)
+  if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   if (n > 1) {
     // a few rows are cut into many partials, many rows into two or three

@@ -1,4 +1,4 @@
-// tmap.h -- host-side encoding of 2-D TMA tensor maps through the driver entry
+// tmap.h -- host-side encoding of 2-D and 3-D TMA tensor maps through the driver entry
 // point (no link-time dependency on libcuda).
 #pragma once
 
@@ -13,5 +13,10 @@ namespace dsa {
 bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                   uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                   uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
+// The same for three dimensions, innermost first; strides in bytes of the
+// second and third dimension.
+bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, const uint64_t dims[3],
+                  const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle);
 
 }  // namespace dsa
