@@ -62,29 +62,30 @@ constexpr int kPBytes = 128 * kSub * 2;             // P: 128 heads x 64 slots, 
 constexpr uint32_t kMsgBytes = kPBytes + 3 * 512;   // then alpha, l, m per head
 // ---- CTA 0 shared memory
 constexpr int kQ8Off = 0;
-constexpr int kKSlotBlocks = 3;                     // a ring slot: 64 slots x three 64-column blocks
-constexpr int kKSlotBytes = kKSlotBlocks * kVBlockBytes;
-constexpr int kKSlots = 6;
+constexpr int kKSlotBytes = kChunk * 128;           // ring place kb: block kb of a chunk's 128 rows
+constexpr int kKSlots = kKB;
 constexpr int kKRingOff = kQBlockBytes;
 constexpr int kStages = 3;
 constexpr int kStageOff = kKRingOff + kKSlots * kKSlotBytes;      // 163840
 constexpr int kMaxOff = kStageOff + kStages * (int)kMsgBytes;     // 217600: maxima [2][2][128]
 constexpr int kMaskOff = kMaxOff + 2 * 2 * 128 * 4;               // validity words [4][4]
-constexpr int kQkEnd = kMaskOff + 4 * 16;
+constexpr int kBoxOff = kMaskOff + 4 * 16;                        // row coordinates [8]
+constexpr int kQkEnd = kBoxOff + 8 * 4;
 // ---- CTA 1 shared memory
 constexpr int kVSlotBytes = kSub * 512;             // 64 slots x 256 columns
 constexpr int kVSlots = 5;
 constexpr int kPBufs = 3;
 constexpr int kPOff = kVSlots * kVSlotBytes;                      // 163840
 constexpr int kOutOff = kPOff + kPBufs * (int)kMsgBytes;          // 217600: epilogue staging, 1 KB per warp
-constexpr int kPvEnd = kOutOff + 8 * 1024;
+constexpr int kPvBoxOff = kOutOff + 8 * 1024;
+constexpr int kPvEnd = kPvBoxOff + 4 * 4;
 // ---- both
 constexpr int kBarOff = (kQkEnd > kPvEnd ? kQkEnd : kPvEnd);
 enum Bar : int {
   kQFull = 0,                       // CTA 0: query block 8 has landed
   kQFree,                           // CTA 0: the products of a part are complete
-  kKFull,                           // [6] CTA 0
-  kKEmpty = kKFull + kKSlots,       // [6] CTA 0
+  kKFull,                           // [9] CTA 0
+  kKEmpty = kKFull + kKSlots,       // [9] CTA 0
   kSFull = kKEmpty + kKSlots,       // [2] CTA 0
   kSEmpty = kSFull + 2,             // [2] CTA 0
   kMaskFull = kSEmpty + 2,          // [4] CTA 0: the chunk's validity words are written
@@ -109,7 +110,7 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBarOff % 8 == 0 && kMiscOff % 8 == 0 && kMsgBytes % 16 == 0 && kStageOff % 128 == 0 && kPOff % 128 == 0, "alignment");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // CTA 0: query blocks 0-7 in [0, 256), S buffers at 256 and 384
-constexpr uint32_t kIdescQK = idesc_bf16(128, kSub);
+constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
 
 // A row that part boundaries cut, as the combine kernel sees it.
@@ -312,7 +313,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
       // ---- the chunks' blocks: lane i < 2 * nbox64 locates box i
       const uint32_t on = elect_one();
-      uint32_t g = 0, ring = 0, item = 0;  // chunk, block and part counters
+      uint32_t g = 0, item = 0;  // chunks and parts so far
+      int32_t* const yk = reinterpret_cast<int32_t*>(smem + kBoxOff);  // row coordinates of a chunk's boxes
+      int q_sent = 0, k_sent = 0;  // blocks of the current part's query, of the current chunk
       bool ok = true;
       while (ok && wk.next(p)) {
         if (wk.bad && lane == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
@@ -337,15 +340,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int32_t y = 0, y_next = 0;
         int valid = 0, valid_next = 0;
         locate(wk.lo, y, valid);
-        // the query's blocks 0-7 go through the ring, on their way to TMEM
+        // The query's blocks 0-7 go through the ring's places 0-7, on their
+        // way to TMEM: those places serve one block more per part.
 #pragma unroll 1
-        for (int kb = 0; kb < kKB - 1; ++kb, ++ring) {
-          const uint32_t slot = ring % kKSlots;
-          if (!(ok = warp_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
+        for (int kb = 0; ok && kb < kKB - 1; ++kb) {
+          if (!(ok = warp_wait(bar(kKEmpty + kb), (g + item + 1) & 1, abort, p.wait_limit_ns))) break;
           if (on) {
-            mbar_arrive_expect_tx(bar(kKFull + slot), kQBlockBytes);
-            tma_load_2d(sbase + kKRingOff + slot * kKSlotBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + slot));
+            mbar_arrive_expect_tx(bar(kKFull + kb), kQBlockBytes);
+            tma_load_2d(sbase + kKRingOff + kb * kKSlotBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + kb));
           }
+          __syncwarp();
+          q_sent = kb + 1;
         }
         if (!ok) break;
         if (item > 0 && !(ok = warp_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns))) break;
@@ -354,6 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.row * p.H, bar(kQFull));
         }
         ++item;
+        q_sent = 0;
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           // validity words of the chunk, 16 slots (never more than a box) at a time
           uint32_t word = 0;
@@ -367,45 +373,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
           if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
-          int32_t yb[8];
-#pragma unroll
-          for (int bx = 0; bx < 8; ++bx) yb[bx] = __shfl_sync(0xffffffffu, y, bx);
+          if (lane < 8) yk[lane] = y;
+          __syncwarp();
 #pragma unroll 1
-          for (int part = 0; part < 2 * (kKB / kKSlotBlocks); ++part, ++ring) {
-            const uint32_t slot = ring % kKSlots;
-            if (!(ok = warp_wait(bar(kKEmpty + slot), ((ring / kKSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
-            const bool second = part >= kKB / kKSlotBlocks;
-            const int kb = kKSlotBlocks * (second ? part - kKB / kKSlotBlocks : part);
+          for (int kb = 0; kb < kKB; ++kb) {
+            if (!(ok = warp_wait(bar(kKEmpty + kb), (g + (kb < kKB - 1 ? item : 0) + 1) & 1, abort, p.wait_limit_ns))) break;
             if (on) {
-              const uint32_t dst = sbase + kKRingOff + slot * kKSlotBytes, full = bar(kKFull + slot);
+              const uint32_t full = bar(kKFull + kb);
+              uint32_t dst = sbase + kKRingOff + kb * kKSlotBytes;
               mbar_arrive_expect_tx(full, kKSlotBytes);
-              if (p.box == 64) {
-                tma_load_3d(dst, &tm_k, 0, second ? yb[1] : yb[0], kb, full);
-              } else if (p.box == 32) {
-#pragma unroll
-                for (int bx = 0; bx < 2; ++bx)
-#pragma unroll
-                  for (int blk = 0; blk < kKSlotBlocks; ++blk)
-                    tma_load_2d(dst + blk * kVBlockBytes + bx * 32 * 128, &tm_k, (kb + blk) * 64, second ? yb[2 + bx] : yb[bx], full);
-              } else {
-#pragma unroll
-                for (int bx = 0; bx < 4; ++bx)
-#pragma unroll
-                  for (int blk = 0; blk < kKSlotBlocks; ++blk)
-                    tma_load_2d(dst + blk * kVBlockBytes + bx * 16 * 128, &tm_k, (kb + blk) * 64, second ? yb[4 + bx] : yb[bx], full);
+#pragma unroll 1
+              for (int bx = 0; bx < nbox; bx += 2, dst += 2 * p.box * 128) {
+                tma_load_2d(dst, &tm_k, kb * 64, yk[bx], full);
+                tma_load_2d(dst + p.box * 128, &tm_k, kb * 64, yk[bx + 1], full);
               }
             }
             __syncwarp();
+            k_sent = kb + 1;
           }
+          if (!ok) break;  // before g counts a chunk that was not sent
+          k_sent = 0;
           y = y_next;
           valid = valid_next;
         }
       }
       if (*abort) {
         give_up();
-        volatile int never = 0;  // the loads in flight must land before the CTA exits
-        for (uint32_t k = ring > kKSlots ? ring - kKSlots : 0; k < ring; ++k)
-          mbar_wait(bar(kKFull + k % kKSlots), (k / kKSlots) & 1, &never, 10000000ull);
+        // The loads in flight must land before the CTA exits: wait (10 ms at
+        // most) for the last fill of every place.  Uses of place kb so far:
+        // chunks, and for places 0-7 parts.
+        volatile int never = 0;
+        for (int kb = 0; kb < kKB; ++kb) {
+          uint32_t uses = g + (kb < k_sent ? 1u : 0u);
+          if (kb < kKB - 1) uses += item + (kb < q_sent ? 1u : 0u);
+          if (uses > 0) mbar_wait(bar(kKFull + kb), (uses - 1) & 1, &never, 10000000ull);
+        }
         if (item > 0) mbar_wait(bar(kQFull), (item - 1) & 1, &never, 10000000ull);
       }
     } else if (warp == kMmaWarp) {
@@ -418,21 +420,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return there;
       };
-      uint32_t g = 0, ring = 0, item = 0;
+      uint32_t g = 0, item = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
         if (wk.lo >= wk.hi) continue;
         // the query into TMEM, once no product reads the one before
         if (item > 0 && !(ok = wait(kQFree, (item - 1) & 1))) break;
 #pragma unroll 1
-        for (int kb = 0; kb < kKB - 1; ++kb, ++ring) {
-          const uint32_t slot = ring % kKSlots;
-          if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
+        for (int kb = 0; kb < kKB - 1; ++kb) {
+          if (!(ok = wait(kKFull + kb, (g + item) & 1))) break;
           if (on) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((slot * kKSlotBytes) >> 4) + (uint64_t)ks * 2);
-            tc_commit(bar(kKEmpty + slot));
+              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((kb * kKSlotBytes) >> 4) + (uint64_t)ks * 2);
+            tc_commit(bar(kKEmpty + kb));
           }
           __syncwarp();
         }
@@ -441,27 +442,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(kSEmpty + sb, ((g - 2) >> 1) & 1))) break;
-          for (int half = 0; ok && half < 2; ++half) {
-            const uint32_t d = tmem + kTmemS + 128 * sb + 64 * half;
+          const uint32_t d = tmem + kTmemS + 128 * sb;
+#pragma unroll 1
+          for (int kb = 0; kb < kKB - 1; ++kb) {
+            if (!(ok = wait(kKFull + kb, (g + item) & 1))) break;
+            const uint64_t bs = kb0 + (uint64_t)((kb * kKSlotBytes) >> 4);
 #pragma unroll
-            for (int part = 0; part < kKB / kKSlotBlocks; ++part, ++ring) {
-              const uint32_t slot = ring % kKSlots;
-              if (!(ok = wait(kKFull + slot, (ring / kKSlots) & 1))) break;
-              const uint64_t bs = kb0 + (uint64_t)((slot * kKSlotBytes) >> 4);
-#pragma unroll
-              for (int blk = 0; blk < kKSlotBlocks; ++blk) {
-                const int kb = kKSlotBlocks * part + blk;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                  const uint64_t bd = bs + (uint64_t)((blk * kVBlockBytes) >> 4) + (uint64_t)ks * 2;
-                  if (kb < kKB - 1) mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bd, kIdescQK, (kb | ks) ? 1u : 0u);
-                  else mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bd, kIdescQK, 1u);
-                }
-              }
-              if (on) tc_commit(bar(kKEmpty + slot));
-            }
+            for (int ks = 0; ks < 4; ++ks)
+              mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
+            if (on) tc_commit(bar(kKEmpty + kb));
           }
-          if (ok && on) tc_commit(bar(kSFull + sb));
+          if (!ok || !(ok = wait(kKFull + kKB - 1, g & 1))) break;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, kb0 + (uint64_t)(((kKB - 1) * kKSlotBytes) >> 4) + (uint64_t)ks * 2, kIdescQK, 1u);
+          if (on) tc_commit(bar(kKEmpty + kKB - 1));
+          if (on) tc_commit(bar(kSFull + sb));
         }
         if (ok && on) tc_commit(bar(kQFree));
       }
@@ -620,6 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ring = 0;
       bool ok = true;
       const uint32_t on = elect_one();
+      int32_t* const yv = reinterpret_cast<int32_t*>(smem + kPvBoxOff);  // row coordinates of a tile's boxes
       while (ok && wk.next(p)) {
         const int b = wk.row / p.T;
         auto locate = [&](int i) -> int32_t {  // i counts 64-slot halves
@@ -634,30 +631,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (wk.lo < wk.hi) y = locate(2 * wk.lo);
         for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i) {
           if (i + 1 < 2 * wk.hi) y_next = locate(i + 1);
-          int32_t yb[4];
-#pragma unroll
-          for (int bx = 0; bx < 4; ++bx) yb[bx] = __shfl_sync(0xffffffffu, y, bx);
-#pragma unroll
+          if (lane < 4) yv[lane] = y;
+          __syncwarp();
+#pragma unroll 1
           for (int n = 0; n < 2; ++n, ++ring) {
             const uint32_t slot = ring % kVSlots;
             if (!(ok = warp_wait(bar(kVEmpty + slot), ((ring / kVSlots) & 1) ^ 1, abort, p.wait_limit_ns))) break;
             if (on) {
               mbar_arrive_expect_tx(bar(kVFull + slot), kVSlotBytes);
-              const uint32_t dst = sbase + slot * kVSlotBytes, full = bar(kVFull + slot);
+              const uint32_t full = bar(kVFull + slot);
+              uint32_t dst = sbase + slot * kVSlotBytes;
               if (p.box == 64) {
-                tma_load_3d(dst, &tm_v, 0, yb[0], 4 * n, full);
-              } else if (p.box == 32) {
-#pragma unroll
-                for (int bx = 0; bx < 2; ++bx)
-#pragma unroll
-                  for (int blk = 0; blk < 4; ++blk)
-                    tma_load_2d(dst + blk * kVBlockBytes + bx * 32 * 128, &tm_v, 256 * n + 64 * blk, yb[bx], full);
+                tma_load_3d(dst, &tm_v, 0, yv[0], 4 * n, full);
               } else {
-#pragma unroll
-                for (int bx = 0; bx < 4; ++bx)
+#pragma unroll 1
+                for (int bx = 0; bx < nbox64; ++bx, dst += p.box * 128) {
 #pragma unroll
                   for (int blk = 0; blk < 4; ++blk)
-                    tma_load_2d(dst + blk * kVBlockBytes + bx * 16 * 128, &tm_v, 256 * n + 64 * blk, yb[bx], full);
+                    tma_load_2d(dst + blk * kVBlockBytes, &tm_v, 256 * n + 64 * blk, yv[bx], full);
+                }
               }
             }
             __syncwarp();
@@ -1054,18 +1046,15 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   CUtensorMap tq, tk, tv;
   const uint64_t rows = (uint64_t)n_pages * page_size;
   bool maps = make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
+                           CU_TENSOR_MAP_SWIZZLE_128B) &&
+              make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, rows, kDQK * 2, 64, (uint32_t)p.box,
                            CU_TENSOR_MAP_SWIZZLE_128B);
-  if (p.box == 64) {
-    // a ring slot is one box: 64 rows of three (K) or four (V) column blocks
+  tv = tk;
+  if (p.box == 64) {  // a tile of V is one box: 64 rows of four column blocks
     const uint64_t dims[3] = {64, rows, kKB}, strides[2] = {kDQK * 2, 128};
-    const uint32_t box_k[3] = {64, 64, kKSlotBlocks}, box_v[3] = {64, 64, 4};
+    const uint32_t box_v[3] = {64, 64, 4};
     maps = maps &&
-           make_tmap_3d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_k, CU_TENSOR_MAP_SWIZZLE_128B) &&
            make_tmap_3d(&tv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_v, CU_TENSOR_MAP_SWIZZLE_128B);
-  } else {
-    maps = maps && make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, rows, kDQK * 2, 64, (uint32_t)p.box,
-                                CU_TENSOR_MAP_SWIZZLE_128B);
-    tv = tk;
   }
   if (!maps) return DSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

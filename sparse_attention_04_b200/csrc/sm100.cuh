@@ -520,53 +520,40 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
-// Looks at a barrier's phase up to `tries` times in a tight loop.
+// try_wait that may suspend the thread for up to kSuspendNs.  Without the hint
+// it comes back after some 70 cycles, and a dozen warps that look again and
+// again keep the unit busy that serves every mbarrier and shared-memory
+// access of the SM: the MMA warp's own waits then took 300 to 900 cycles.
+constexpr uint32_t kSuspendNs = 10000u;
 template <bool kCluster>
-__device__ __forceinline__ uint32_t mbar_try_wait_n(uint32_t bar, uint32_t parity, uint32_t tries) {
+__device__ __forceinline__ bool mbar_try_wait_suspend(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   if (kCluster)
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, %3;\n"
-        "AGAIN:\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra AGAIN;\n"
-        "DONE:\n\t"
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(tries)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, %3;\n"
-        "AGAIN:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra AGAIN;\n"
-        "DONE:\n\t"
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(tries)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
-  return ok;
+  return ok != 0;
 }
 
-// mbar_wait by a whole converged warp: every lane gets the same answer.  The
-// clock and the abort flag are looked at only once per 256 tries, so that a
-// wait costs about 60 cycles where the phase is over (mbar_wait and a vote:
-// 116).  A try takes about 70 cycles: the bound is limit_ns plus two rounds.
+// mbar_wait by a whole converged warp: every lane gets the same answer.
 template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-  if (__all_sync(0xffffffffu, mbar_try_wait_n<kCluster>(bar, parity, 256u))) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait_suspend<kCluster>(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_n<kCluster>(bar, parity, 256u))) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait_suspend<kCluster>(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > limit_ns)) {
       *abort = 1;
       return false;
