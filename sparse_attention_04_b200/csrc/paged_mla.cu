@@ -62,8 +62,10 @@ constexpr int kPBytes = 128 * kSub * 2;             // P: 128 heads x 64 slots, 
 constexpr uint32_t kMsgBytes = kPBytes + 3 * 512;   // then alpha, l, m per head
 // ---- CTA 0 shared memory
 constexpr int kQ8Off = 0;
-constexpr int kKSlotBytes = kChunk * 128;           // ring place kb: block kb of a chunk's 128 rows
-constexpr int kKSlots = kKB;
+constexpr int kKBlockBytes = kChunk * 128;          // a 64-column block of a chunk's 128 rows
+constexpr int kKSlotBlocks = 3;                     // ring place i: blocks 3i .. 3i + 2 of a chunk
+constexpr int kKSlotBytes = kKSlotBlocks * kKBlockBytes;
+constexpr int kKSlots = kKB / kKSlotBlocks;
 constexpr int kKRingOff = kQBlockBytes;
 constexpr int kStages = 3;
 constexpr int kStageOff = kKRingOff + kKSlots * kKSlotBytes;      // 163840
@@ -84,8 +86,8 @@ constexpr int kBarOff = (kQkEnd > kPvEnd ? kQkEnd : kPvEnd);
 enum Bar : int {
   kQFull = 0,                       // CTA 0: query block 8 has landed
   kQFree,                           // CTA 0: the products of a part are complete
-  kKFull,                           // [9] CTA 0
-  kKEmpty = kKFull + kKSlots,       // [9] CTA 0
+  kKFull,                           // [3] CTA 0
+  kKEmpty = kKFull + kKSlots,       // [3] CTA 0
   kSFull = kKEmpty + kKSlots,       // [2] CTA 0
   kSEmpty = kSFull + 2,             // [2] CTA 0
   kMaskFull = kSEmpty + 2,          // [4] CTA 0: the chunk's validity words are written
@@ -315,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t on = elect_one();
       uint32_t g = 0, item = 0;  // chunks and parts so far
       int32_t* const yk = reinterpret_cast<int32_t*>(smem + kBoxOff);  // row coordinates of a chunk's boxes
-      int q_sent = 0, k_sent = 0;  // blocks of the current part's query, of the current chunk
+      int sent = 0;  // places filled for the current query or chunk
       bool ok = true;
       while (ok && wk.next(p)) {
         if (wk.bad && lane == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
@@ -340,17 +342,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int32_t y = 0, y_next = 0;
         int valid = 0, valid_next = 0;
         locate(wk.lo, y, valid);
-        // The query's blocks 0-7 go through the ring's places 0-7, on their
-        // way to TMEM: those places serve one block more per part.
+        // the query's blocks 0-7 go through the ring, on their way to TMEM
 #pragma unroll 1
-        for (int kb = 0; ok && kb < kKB - 1; ++kb) {
-          if (!(ok = warp_wait(bar(kKEmpty + kb), (g + item + 1) & 1, abort, p.wait_limit_ns))) break;
+        for (int pl = 0; pl < kKSlots; ++pl) {
+          if (!(ok = warp_wait(bar(kKEmpty + pl), (g + item + 1) & 1, abort, p.wait_limit_ns))) break;
           if (on) {
-            mbar_arrive_expect_tx(bar(kKFull + kb), kQBlockBytes);
-            tma_load_2d(sbase + kKRingOff + kb * kKSlotBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + kb));
+            const int kb0 = kKSlotBlocks * pl, kb1 = min(kb0 + kKSlotBlocks, kKB - 1);
+            mbar_arrive_expect_tx(bar(kKFull + pl), (kb1 - kb0) * kQBlockBytes);
+            for (int kb = kb0; kb < kb1; ++kb)
+              tma_load_2d(sbase + kKRingOff + kb * kKBlockBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + pl));
           }
           __syncwarp();
-          q_sent = kb + 1;
+          sent = pl + 1;
         }
         if (!ok) break;
         if (item > 0 && !(ok = warp_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns))) break;
@@ -359,15 +362,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.row * p.H, bar(kQFull));
         }
         ++item;
-        q_sent = 0;
+        sent = 0;
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           // validity words of the chunk, 16 slots (never more than a box) at a time
-          uint32_t word = 0;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int k0 = 32 * (lane & 3) + 16 * hh, bx = k0 / p.box;
-            const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
-            word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
+          uint32_t word = ~0u;
+          if (!__all_sync(0xffffffffu, lane >= nbox || valid == p.box)) {
+            word = 0;
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              const int k0 = 32 * (lane & 3) + 16 * hh, bx = k0 / p.box;
+              const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
+              word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
+            }
           }
           if (lane < 4) reinterpret_cast<uint32_t*>(smem + kMaskOff)[4 * (g & 3) + lane] = word;
           __syncwarp();
@@ -376,23 +382,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane < 8) yk[lane] = y;
           __syncwarp();
 #pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) {
-            if (!(ok = warp_wait(bar(kKEmpty + kb), (g + (kb < kKB - 1 ? item : 0) + 1) & 1, abort, p.wait_limit_ns))) break;
+          for (int pl = 0; pl < kKSlots; ++pl) {
+            if (!(ok = warp_wait(bar(kKEmpty + pl), (g + item + 1) & 1, abort, p.wait_limit_ns))) break;
             if (on) {
-              const uint32_t full = bar(kKFull + kb);
-              uint32_t dst = sbase + kKRingOff + kb * kKSlotBytes;
+              const uint32_t full = bar(kKFull + pl);
+              uint32_t dst = sbase + kKRingOff + pl * kKSlotBytes;
               mbar_arrive_expect_tx(full, kKSlotBytes);
 #pragma unroll 1
-              for (int bx = 0; bx < nbox; bx += 2, dst += 2 * p.box * 128) {
-                tma_load_2d(dst, &tm_k, kb * 64, yk[bx], full);
-                tma_load_2d(dst + p.box * 128, &tm_k, kb * 64, yk[bx + 1], full);
+              for (int bx = 0; bx < nbox; ++bx, dst += p.box * 128) {
+                const int32_t yy = yk[bx];
+#pragma unroll
+                for (int blk = 0; blk < kKSlotBlocks; ++blk)
+                  tma_load_2d(dst + blk * kKBlockBytes, &tm_k, (kKSlotBlocks * pl + blk) * 64, yy, full);
               }
             }
             __syncwarp();
-            k_sent = kb + 1;
+            sent = pl + 1;
           }
           if (!ok) break;  // before g counts a chunk that was not sent
-          k_sent = 0;
+          sent = 0;
           y = y_next;
           valid = valid_next;
         }
@@ -400,13 +408,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (*abort) {
         give_up();
         // The loads in flight must land before the CTA exits: wait (10 ms at
-        // most) for the last fill of every place.  Uses of place kb so far:
-        // chunks, and for places 0-7 parts.
+        // most) for the last fill of every place (one per chunk and per part).
         volatile int never = 0;
-        for (int kb = 0; kb < kKB; ++kb) {
-          uint32_t uses = g + (kb < k_sent ? 1u : 0u);
-          if (kb < kKB - 1) uses += item + (kb < q_sent ? 1u : 0u);
-          if (uses > 0) mbar_wait(bar(kKFull + kb), (uses - 1) & 1, &never, 10000000ull);
+        for (int pl = 0; pl < kKSlots; ++pl) {
+          const uint32_t fills = g + item + (pl < sent ? 1u : 0u);
+          if (fills > 0) mbar_wait(bar(kKFull + pl), (fills - 1) & 1, &never, 10000000ull);
         }
         if (item > 0) mbar_wait(bar(kQFull), (item - 1) & 1, &never, 10000000ull);
       }
@@ -427,13 +433,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the query into TMEM, once no product reads the one before
         if (item > 0 && !(ok = wait(kQFree, (item - 1) & 1))) break;
 #pragma unroll 1
-        for (int kb = 0; kb < kKB - 1; ++kb) {
-          if (!(ok = wait(kKFull + kb, (g + item) & 1))) break;
+        for (int pl = 0; pl < kKSlots; ++pl) {
+          if (!(ok = wait(kKFull + pl, (g + item) & 1))) break;
           if (on) {
+            for (int kb = kKSlotBlocks * pl; kb < min(kKSlotBlocks * (pl + 1), kKB - 1); ++kb)
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((kb * kKSlotBytes) >> 4) + (uint64_t)ks * 2);
-            tc_commit(bar(kKEmpty + kb));
+              for (int ks = 0; ks < 4; ++ks)
+                tmem_cp_128x32b(tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((kb * kKBlockBytes) >> 4) + (uint64_t)ks * 2);
+            tc_commit(bar(kKEmpty + pl));
           }
           __syncwarp();
         }
@@ -444,19 +451,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (g >= 2 && !(ok = wait(kSEmpty + sb, ((g - 2) >> 1) & 1))) break;
           const uint32_t d = tmem + kTmemS + 128 * sb;
 #pragma unroll 1
-          for (int kb = 0; kb < kKB - 1; ++kb) {
-            if (!(ok = wait(kKFull + kb, (g + item) & 1))) break;
-            const uint64_t bs = kb0 + (uint64_t)((kb * kKSlotBytes) >> 4);
+          for (int pl = 0; pl < kKSlots - 1; ++pl) {
+            if (!(ok = wait(kKFull + pl, (g + item) & 1))) break;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bs + (uint64_t)ks * 2, kIdescQK, (kb | ks) ? 1u : 0u);
-            if (on) tc_commit(bar(kKEmpty + kb));
+            for (int u = 0; u < 4 * kKSlotBlocks; ++u) {
+              const int kb = kKSlotBlocks * pl + u / 4, ks = u % 4;
+              mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, kb0 + (uint64_t)((kb * kKBlockBytes) >> 4) + (uint64_t)ks * 2,
+                            kIdescQK, (kb | ks) ? 1u : 0u);
+            }
+            if (on) tc_commit(bar(kKEmpty + pl));
           }
-          if (!ok || !(ok = wait(kKFull + kKB - 1, g & 1))) break;
+          if (!ok || !(ok = wait(kKFull + kKSlots - 1, (g + item) & 1))) break;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, kb0 + (uint64_t)(((kKB - 1) * kKSlotBytes) >> 4) + (uint64_t)ks * 2, kIdescQK, 1u);
-          if (on) tc_commit(bar(kKEmpty + kKB - 1));
+          for (int u = 0; u < 4 * kKSlotBlocks; ++u) {
+            const int kb = kKB - kKSlotBlocks + u / 4, ks = u % 4;
+            const uint64_t bd = kb0 + (uint64_t)((kb * kKBlockBytes) >> 4) + (uint64_t)ks * 2;
+            if (kb < kKB - 1) mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bd, kIdescQK, 1u);
+            else mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bd, kIdescQK, 1u);
+          }
+          if (on) tc_commit(bar(kKEmpty + kKSlots - 1));
           if (on) tc_commit(bar(kSFull + sb));
         }
         if (ok && on) tc_commit(bar(kQFree));
