@@ -117,53 +117,61 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
 
 // A row that part boundaries cut, as the combine kernel sees it.
 struct CutRow {
-  int row;    // -1: none
+  int q0;     // first row of out; -1: none
   int first;  // cluster of its first partial
   int count;  // partials, one per cluster from `first` on
-  int pad;
+  int m;      // rows
 };
 
 struct PagedMlaParams {
   PagePool pool;
   const int32_t* lens;
-  int n_rows, T, H, n_clusters;
+  int T, H, n_clusters;
+  int tp;            // tokens per tile: as many as 128 rows (token, head) hold
+  int tiles;         // tiles per sequence
+  int n_rows;        // B * tiles
   int box;           // rows per TMA box
   float scale_log2;
   void* out;
   int out_bf16;
   float* lse;
   CutRow* cut;       // [n_clusters]
-  float* part_ml;    // [2 * n_clusters][2][H]: maximum, sum
-  float* part_o;     // [2 * n_clusters][128][H][4], unnormalised
+  float* part_ml;    // [2 * n_clusters][2][tp * H]: maximum, sum
+  float* part_o;     // [2 * n_clusters][128][tp * H][4], unnormalised
   int32_t* status;
   int debug_stall;
   uint64_t wait_limit_ns;
 };
 
-// Slots row r sees.
+// Slots that the last token of tile r sees.
 __device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool& bad) {
-  const int b = r / p.T;
+  const int b = r / p.tiles, t1 = min(p.T, (r - b * p.tiles + 1) * p.tp);
   const int32_t len = checked_len(__ldg(p.lens + b), pool_capacity(p.pool), bad);
-  return max(0, len - p.T + (r - b * p.T) + 1);
+  return max(0, len - p.T + t1);
 }
 __device__ __forceinline__ int64_t n_chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
 
-// One after the other, the parts of rows that fall to this cluster.  Every
+// One after the other, the parts of tiles that fall to this cluster.  Every
 // role of both CTAs walks the same list.
 struct Walk {
   int64_t u;       // first unit of row r
   int64_t w0, w1;  // this cluster's units
   int r, n_rows;
   // of the current part:
-  int row, lo, hi, chunks;
-  int32_t len;
+  int seq, lo, hi, chunks;
+  int q0, nt, m;  // first row of q and out, tokens, rows (token, head)
+  int32_t len;    // slots the tile's last token sees
   bool bad;
 
   __device__ __forceinline__ bool next(const PagedMlaParams& p) {
     while (r < n_rows && u < w1) {
       len = row_len(p, r, bad);
       const int64_t c = n_chunks_of(len), u0 = u + kRowUnits;
-      row = r;
+      seq = r / p.tiles;
+      const int t0 = (r - seq * p.tiles) * p.tp;
+      q0 = (seq * p.T + t0) * p.H;
+      nt = min(p.tp, p.T - t0);
+      m = nt * p.H;
       chunks = (int)c;
       const bool starts_here = u >= w0;
       lo = (int)min(max(w0 - u0, (int64_t)0), c);
@@ -294,14 +302,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // this cluster's boundary cuts a row: the boundary behind the row's first
     // partial describes the row to the combine kernel
     CutRow c{-1, 0, 0, 0};
-    if (wk.r < p.n_rows) {
-      bool bad;
-      const int64_t n = n_chunks_of(row_len(p, wk.r, bad)), u0 = wk.u + kRowUnits;
-      if (wk.w0 > u0 && wk.w0 - share <= u0) {
-        c.row = wk.r;
-        c.first = (int)(u0 / share);
-        c.count = (int)((u0 + n - 1) / share) - c.first + 1;
-      }
+    Walk first = wk;
+    const int64_t u0 = wk.u + kRowUnits;
+    if (first.next(p) && wk.w0 > u0 && wk.w0 - share <= u0) {
+      c.q0 = first.q0;
+      c.first = (int)(u0 / share);
+      c.count = (int)((u0 + first.chunks - 1) / share) - c.first + 1;
+      c.m = first.m;
     }
     p.cut[cl] = c;
   }
@@ -322,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && wk.next(p)) {
         if (wk.bad && lane == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
         if (wk.lo >= wk.hi) continue;
-        const int b = wk.row / p.T;
+        const int b = wk.seq;
         const int nbox = 2 * nbox64;
         // row coordinate and valid slots of this lane's box of chunk i
         auto locate = [&](int i, int32_t& y, int& valid) {
@@ -350,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int kb0 = kKSlotBlocks * pl, kb1 = min(kb0 + kKSlotBlocks, kKB - 1);
             mbar_arrive_expect_tx(bar(kKFull + pl), (kb1 - kb0) * kQBlockBytes);
             for (int kb = kb0; kb < kb1; ++kb)
-              tma_load_2d(sbase + kKRingOff + kb * kKBlockBytes, &tm_q, kb * 64, wk.row * p.H, bar(kKFull + pl));
+              tma_load_2d(sbase + kKRingOff + kb * kKBlockBytes, &tm_q, kb * 64, wk.q0, bar(kKFull + pl));
           }
           __syncwarp();
           sent = pl + 1;
@@ -359,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (item > 0 && !(ok = warp_wait(bar(kQFree), (item - 1) & 1, abort, p.wait_limit_ns))) break;
         if (on) {
           mbar_arrive_expect_tx(bar(kQFull), kQBlockBytes);
-          tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.row * p.H, bar(kQFull));
+          tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, wk.q0, bar(kQFull));
         }
         ++item;
         sent = 0;
@@ -389,11 +396,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t dst = sbase + kKRingOff + pl * kKSlotBytes;
               mbar_arrive_expect_tx(full, kKSlotBytes);
 #pragma unroll 1
-              for (int bx = 0; bx < nbox; ++bx, dst += p.box * 128) {
-                const int32_t yy = yk[bx];
+              for (int bx = 0; bx < nbox; bx += 2, dst += 2 * p.box * 128) {
+                const int32_t ya = yk[bx], yb = yk[bx + 1];
 #pragma unroll
-                for (int blk = 0; blk < kKSlotBlocks; ++blk)
-                  tma_load_2d(dst + blk * kKBlockBytes, &tm_k, (kKSlotBlocks * pl + blk) * 64, yy, full);
+                for (int blk = 0; blk < kKSlotBlocks; ++blk) {
+                  tma_load_2d(dst + blk * kKBlockBytes, &tm_k, (kKSlotBlocks * pl + blk) * 64, ya, full);
+                  tma_load_2d(dst + blk * kKBlockBytes + p.box * 128, &tm_k, (kKSlotBlocks * pl + blk) * 64, yb, full);
+                }
               }
             }
             __syncwarp();
@@ -526,10 +535,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < 8) {
       // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
       const int h = (warp & 3) * 32 + lane, half = warp >> 2;
-      const bool dead = (warp & 3) * 32 >= p.H;  // a warp without heads only keeps step
       uint32_t g = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
+        const bool dead = (warp & 3) * 32 >= wk.m;  // a warp without rows only keeps step
+        // slots that this row's token sees, and the tile's first token
+        const int row_len = wk.len - max(0, wk.nt - 1 - h / p.H), min_len = wk.len - (wk.nt - 1);
         float m_run = -INFINITY, l_run = 0.f;
         for (int i = wk.lo; i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
@@ -546,8 +557,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             const uint32_t* vm = reinterpret_cast<const uint32_t*>(smem + kMaskOff) + 4 * (g & 3) + 2 * half;
-            const uint32_t vm0 = vm[0], vm1 = vm[1];
+            uint32_t vm0 = vm[0], vm1 = vm[1];
             warp_arrive(bar(kSEmpty + sb));
+            const int64_t s0 = (int64_t)i * kChunk + 64 * half;
+            if (s0 + 64 > min_len) {  // the tile's tokens see different slots here
+              const int see = (int)max(row_len - s0, (int64_t)0);
+              vm0 &= see >= 32 ? ~0u : (1u << see) - 1u;
+              vm1 &= see >= 64 ? ~0u : see <= 32 ? 0u : (1u << (see - 32)) - 1u;
+            }
             if (!dead) {
               // x = s * scale * log2(e); masked slots -inf
 #pragma unroll
@@ -631,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t on = elect_one();
       int32_t* const yv = reinterpret_cast<int32_t*>(smem + kPvBoxOff);  // row coordinates of a tile's boxes
       while (ok && wk.next(p)) {
-        const int b = wk.row / p.T;
+        const int b = wk.seq;
         auto locate = [&](int i) -> int32_t {  // i counts 64-slot halves
           const int64_t s = (int64_t)i * kSub + lane * p.box;
           if (lane < nbox64 && s < wk.len) {
@@ -658,10 +675,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_load_3d(dst, &tm_v, 0, yv[0], 4 * n, full);
               } else {
 #pragma unroll 1
-                for (int bx = 0; bx < nbox64; ++bx, dst += p.box * 128) {
+                for (int bx = 0; bx < nbox64; bx += 2, dst += 2 * p.box * 128) {
+                  const int32_t ya = yv[bx], yb = yv[bx + 1];
 #pragma unroll
-                  for (int blk = 0; blk < 4; ++blk)
-                    tma_load_2d(dst + blk * kVBlockBytes, &tm_v, 256 * n + 64 * blk, yv[bx], full);
+                  for (int blk = 0; blk < 4; ++blk) {
+                    tma_load_2d(dst + blk * kVBlockBytes, &tm_v, 256 * n + 64 * blk, ya, full);
+                    tma_load_2d(dst + blk * kVBlockBytes + p.box * 128, &tm_v, 256 * n + 64 * blk, yb, full);
+                  }
                 }
               }
             }
@@ -732,11 +752,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < 8) {
       // ---- rescale and epilogue: thread = (head h, half of the columns)
       const int h = (warp & 3) * 32 + lane, col0 = 256 * (warp >> 2);
-      const bool dead = (warp & 3) * 32 >= p.H;
       uint8_t* const ostage = smem + kOutOff + warp * 1024;
       uint32_t j = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
+        const bool dead = (warp & 3) * 32 >= wk.m;
         float l_half[2] = {0.f, 0.f}, m_row = -INFINITY;
         for (int i = 2 * wk.lo; i < 2 * wk.hi; ++i, ++j) {
           const uint32_t pb = j % kPBufs;
@@ -765,22 +785,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tc_wait_st();
             }
           }
-          // slots behind the row's end that share the last box with it
-          const int64_t left = (int64_t)wk.len - (int64_t)i * kSub;
-          if (left > 0 && left < kSub && left % p.box != 0) {
-            const int z0 = (int)left, z1 = ((int)left + p.box - 1) / p.box * p.box;
+          // Two kinds of slots must not meet the product as they are.  Slots
+          // behind the end that share the last box with it may hold anything:
+          // they become zeros.  Slots that only some of the tile's tokens see
+          // have P = 0 in the others' rows, and 0 * NaN is not 0: a row that is
+          // not finite becomes zeros too (the tokens that see it have a NaN
+          // for a sum already).
+          const int64_t s0 = (int64_t)i * kSub;
+          const int z_end = (int)min((int64_t)kSub, max((int64_t)0, ((int64_t)wk.len + p.box - 1) / p.box * p.box - s0));
+          const int z_begin = (int)min((int64_t)kSub, max((int64_t)0, (int64_t)wk.len - (wk.nt - 1) - s0));
+          if (z_begin < z_end) {
+            const uint32_t k0 = (2 * j) % kVSlots, k1 = (2 * j + 1) % kVSlots;
+            ok = warp_wait(bar(kVFull + k0), ((2 * j) / kVSlots) & 1, abort, p.wait_limit_ns) &&
+                 warp_wait(bar(kVFull + k1), ((2 * j + 1) / kVSlots) & 1, abort, p.wait_limit_ns);
+            if (!ok) break;
+            // a warp takes a row: 2 x 4 blocks x 8 pieces of 16 bytes
+            for (int z = z_begin + warp; z < z_end; z += 8) {
+              uint8_t* const row = smem + (lane >> 3) * kVBlockBytes + z * 128 + (lane & 7) * 16;
+              uint4* const a = reinterpret_cast<uint4*>(row + k0 * kVSlotBytes);
+              uint4* const b = reinterpret_cast<uint4*>(row + k1 * kVSlotBytes);
+              bool clear = s0 + z >= wk.len;
+              if (!clear) {
+                const uint4 va = *a, vb = *b;
+                const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+                bool odd = false;
 #pragma unroll
-            for (uint32_t n = 0; n < 2; ++n) {
-              const uint32_t k = 2 * j + n, slot = k % kVSlots;
-              ok = warp_wait(bar(kVFull + slot), (k / kVSlots) & 1, abort, p.wait_limit_ns);
-              if (!ok) break;
-              for (int e = threadIdx.x; e < (z1 - z0) * 32; e += 256) {  // 4 blocks x 8 pieces of 16 bytes per slot
-                const int z = z0 + (e >> 5), blk = (e >> 3) & 3, c = e & 7;
-                *reinterpret_cast<uint4*>(smem + slot * kVSlotBytes + blk * kVBlockBytes + z * 128 + c * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+                for (int e = 0; e < 8; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                clear = __any_sync(0xffffffffu, odd);
+              }
+              if (clear) {
+                *a = make_uint4(0u, 0u, 0u, 0u);
+                *b = make_uint4(0u, 0u, 0u, 0u);
               }
             }
-            if (!ok) break;
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -800,19 +837,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Partials: [column / 4][head][4], so that a warp's stores are whole
         // lines.  Finished rows: 32 bytes of 32 rows at a time through shared
         // memory, so that two lanes write a row's piece.
-        float4* const pout = reinterpret_cast<float4*>(p.part_o + part * p.H * kDV) + h;
+        const int pm = p.tp * p.H;  // rows a partial has room for
+        float4* const pout = reinterpret_cast<float4*>(p.part_o + part * pm * kDV) + h;
         uint8_t* const rowp = ostage + lane * 32;
         const int sw = (lane >> 2) & 1;
         const int elt = p.out_bf16 ? 2 : 4;
         uint8_t* const gout =
-            reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.row * p.H + (warp & 3) * 32) * (int64_t)(kDV * elt);
+            reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.q0 + (warp & 3) * 32) * (int64_t)(kDV * elt);
         auto flush = [&](int col_byte) {
           __syncwarp();
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int rr = 16 * u + (lane >> 1), c = lane & 1;
             const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 32 + ((c ^ ((rr >> 2) & 1)) << 4));
-            if ((warp & 3) * 32 + rr < p.H)
+            if ((warp & 3) * 32 + rr < wk.m)
               *reinterpret_cast<uint4*>(gout + rr * (kDV * elt) + col_byte + 16 * c) = v;
           }
           __syncwarp();
@@ -830,10 +868,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
           }
           if (!whole) {
-            if (h < p.H) {
+            if (h < wk.m) {
 #pragma unroll
               for (int c = 0; c < 8; ++c)
-                pout[(int64_t)(c0 / 4 + c) * p.H] =
+                pout[(int64_t)(c0 / 4 + c) * pm] =
                     make_float4(__uint_as_float(ov[4 * c]), __uint_as_float(ov[4 * c + 1]), __uint_as_float(ov[4 * c + 2]),
                                 __uint_as_float(ov[4 * c + 3]));
             }
@@ -865,12 +903,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();  // O is read: the next row's first product (after Ready) may overwrite it
-        if (h < p.H && col0 == 0) {
+        if (h < wk.m && col0 == 0) {
           if (whole) {
-            if (p.lse) p.lse[(int64_t)wk.row * p.H + h] = l == 0.f ? -INFINITY : (m_row + log2f(l)) * 0.69314718055994531f;
+            if (p.lse) p.lse[(int64_t)wk.q0 + h] = l == 0.f ? -INFINITY : (m_row + log2f(l)) * 0.69314718055994531f;
           } else {
-            p.part_ml[2 * part * p.H + h] = m_row;
-            p.part_ml[(2 * part + 1) * p.H + h] = l;
+            p.part_ml[2 * part * pm + h] = m_row;
+            p.part_ml[(2 * part + 1) * pm + h] = l;
           }
         }
       }
@@ -899,7 +937,7 @@ constexpr int kMaxClusters = 128;
 template <int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
-                             const float4* __restrict__ part_o, int n_clusters, int H, void* out, int out_bf16, float* lse) {
+                             const float4* __restrict__ part_o, int n_clusters, int pm, void* out, int out_bf16, float* lse) {
   constexpr int kQuads = kCombineWarps / SPLIT;  // column quads per task
   __shared__ CutRow s_cut[kMaxClusters];
   __shared__ int s_n;
@@ -912,14 +950,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     for (int c0 = 0; c0 < n_clusters; c0 += 32) {
       CutRow c{-1, 0, 0, 0};
       if (c0 + lane < n_clusters) c = cut[c0 + lane];
-      const uint32_t m = __ballot_sync(0xffffffffu, c.row >= 0);
-      if (c.row >= 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = c;
+      const uint32_t m = __ballot_sync(0xffffffffu, c.q0 >= 0);
+      if (c.q0 >= 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = c;
       n += __popc(m);
     }
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int hgroups = (H + 31) / 32, per_row = hgroups * (kDV / 4 / kQuads);
+  const int hgroups = (pm + 31) / 32, per_row = hgroups * (kDV / 4 / kQuads);
   const int tasks = s_n * per_row;
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
     const CutRow c = s_cut[task / per_row];
@@ -929,15 +967,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     auto part = [&](int i) -> int64_t { return 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0); };
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
-    if (h < H) {
+    if (h < c.m) {
 #pragma unroll 8
-      for (int i = 0; i < c.count; ++i) M = fmaxf(M, __ldg(part_ml + 2 * part(i) * H + h));
+      for (int i = 0; i < c.count; ++i) M = fmaxf(M, __ldg(part_ml + 2 * part(i) * pm + h));
       const float off = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
       for (int i = sub; i < c.count; i += SPLIT) {
-        const float4 o = __ldg(part_o + (part(i) * (kDV / 4) + quad) * H + h);
-        const float w = exp2f(__ldg(part_ml + 2 * part(i) * H + h) - off);
-        l = fmaf(w, __ldg(part_ml + (2 * part(i) + 1) * H + h), l);
+        const float4 o = __ldg(part_o + (part(i) * (kDV / 4) + quad) * pm + h);
+        const float w = exp2f(__ldg(part_ml + 2 * part(i) * pm + h) - off);
+        l = fmaf(w, __ldg(part_ml + (2 * part(i) + 1) * pm + h), l);
         a.x = fmaf(w, o.x, a.x);
         a.y = fmaf(w, o.y, a.y);
         a.z = fmaf(w, o.z, a.z);
@@ -962,10 +1000,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
         l += s_sum[warp + u][4][lane];
       }
     }
-    if (h >= H) continue;
+    if (h >= c.m) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    const int64_t rh = (int64_t)c.row * H + h;
+    const int64_t rh = (int64_t)c.q0 + h;
     if (out_bf16) {
       const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
       reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[quad] =
@@ -1008,9 +1046,12 @@ int paged_clusters() {
   return e == cudaSuccess ? count[dev] : half;
 }
 
-size_t paged_workspace(int H) {
-  const size_t n = (size_t)paged_clusters();
-  return n * sizeof(CutRow) + 2 * n * H * 2 * sizeof(float) + 2 * n * H * kDV * sizeof(float);
+// Tokens whose (token, head) rows fit in one tile.
+int tokens_per_tile(int T, int H) { return std::max(1, std::min(T, 128 / H)); }
+
+size_t paged_workspace(int T, int H) {
+  const size_t n = (size_t)paged_clusters(), m = (size_t)tokens_per_tile(T, H) * H;
+  return n * sizeof(CutRow) + 2 * n * m * 2 * sizeof(float) + 2 * n * m * kDV * sizeof(float);
 }
 
 }  // namespace
@@ -1022,7 +1063,7 @@ extern "C" {
 
 size_t dsa_paged_mla_workspace_size(int B, int T, int H) {
   if (B <= 0 || T <= 0 || (int64_t)B * T > (int64_t)1 << 24 || H < 1 || H > DSA_MAX_HEADS) return 0;
-  return paged_workspace(H);
+  return paged_workspace(T, H);
 }
 
 int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,
@@ -1033,7 +1074,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_INVALID_ARG;
   if (!(scale == scale) || !is_aligned16(q) || !is_aligned16(out)) return DSA_ERR_INVALID_ARG;
-  const size_t need = paged_workspace(H);
+  const size_t need = paged_workspace(T, H);
   if (!workspace || ws_bytes < need || !is_aligned16(workspace)) return DSA_ERR_WORKSPACE;
   MlaParams debug;
   take_attention_debug(debug);
@@ -1041,9 +1082,11 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   PagedMlaParams p;
   p.pool = PagePool{page_table, ld_table, n_pages, max_pages, page_size};
   p.lens = lens;
-  p.n_rows = B * T;
   p.T = T;
   p.H = H;
+  p.tp = tokens_per_tile(T, H);
+  p.tiles = (T + p.tp - 1) / p.tp;
+  p.n_rows = B * p.tiles;
   p.n_clusters = n;
   p.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1052,7 +1095,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.lse = lse;
   p.cut = reinterpret_cast<CutRow*>(workspace);
   p.part_o = reinterpret_cast<float*>(p.cut + n);
-  p.part_ml = p.part_o + (size_t)2 * n * H * kDV;
+  p.part_ml = p.part_o + (size_t)2 * n * p.tp * H * kDV;
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
   p.wait_limit_ns = debug.wait_limit_ns;
@@ -1076,11 +1119,11 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (n > 1) {
     // a few rows are cut into many partials, many rows into two or three
     const bool few = p.n_rows <= 4;
-    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * ((H + 31) / 32) * (kDV / 4) * (few ? 4 : 1) / kCombineWarps;
+    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * ((p.tp * H + 31) / 32) * (kDV / 4) * (few ? 4 : 1) / kCombineWarps;
     const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * kCombineWarps);
     const auto kernel = few ? paged_mla_combine_kernel<4> : paged_mla_combine_kernel<1>;
     if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml,
-                   reinterpret_cast<const float4*>(p.part_o), n, H, out, p.out_bf16, lse) != cudaSuccess)
+                   reinterpret_cast<const float4*>(p.part_o), n, p.tp * H, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;
   }
   return DSA_OK;
