@@ -11,7 +11,7 @@
 // Split.  The rows' 128-slot chunks form one list; every cluster of two CTAs
 // takes an equal, contiguous part of it, whatever the sequences' lengths
 // (they are read on the device).  A row that lies in one cluster's part is
-// finished there; a row cut by part boundaries leaves one fp32 partial per
+// finished there; a row cut by part boundaries leaves one partial per
 // cluster, joined by paged_mla_combine_kernel.  At most two partials per
 // cluster exist (the row that begins before its part, the row that goes on
 // behind it).
@@ -37,6 +37,7 @@
 // but they may hold NaN) and masked in CTA 0.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -104,7 +105,7 @@ enum Bar : int {
 constexpr int kMiscOff = kBarOff + kNumBar * 8;
 struct Misc {
   int tmem_base, abort, first_row, pad;
-  int64_t first_unit, total_units;
+  int64_t first_unit, total_units, share;
   int64_t warp_sum[kThreads / 32];
 };
 constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
@@ -137,7 +138,8 @@ struct PagedMlaParams {
   float* lse;
   CutRow* cut;       // [n_clusters]
   float* part_ml;    // [2 * n_clusters][2][tp * H]: maximum, sum
-  float* part_o;     // [2 * n_clusters][128][tp * H][4], unnormalised
+  float* part_sc;    // [2 * n_clusters][2][tp * H]: what the columns 0-255 and 256-511 are to be multiplied by
+  uint4* part_o;     // [2 * n_clusters][64][tp * H][8] fp16, unnormalised
   int32_t* status;
   int debug_stall;
   uint64_t wait_limit_ns;
@@ -150,6 +152,13 @@ __device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool&
   return max(0, len - p.T + t1);
 }
 __device__ __forceinline__ int64_t n_chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
+
+// ceil(a / b); the quotient in 32 bits where they hold it (a 64-bit division
+// takes a few hundred cycles).
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int b) {
+  const int64_t n = a + b - 1;
+  return n < ((int64_t)1 << 31) ? (int64_t)((uint32_t)n / (uint32_t)b) : n / b;
+}
 
 // One after the other, the parts of tiles that fall to this cluster.  Every
 // role of both CTAs walks the same list.
@@ -268,10 +277,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (w < warp) before += v;
       total += v;
     }
-    const int64_t share = (total + p.n_clusters - 1) / p.n_clusters;
-    const int64_t w0 = share * cl;
+    const int64_t share = ceil_div(total, p.n_clusters), w0 = share * cl;
     if (threadIdx.x == 0) {
       misc->total_units = total;
+      misc->share = share;
       if (w0 >= total) misc->first_row = p.n_rows;
     }
     if (before <= w0 && w0 < before + mine) {  // one thread, if any
@@ -290,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
-  const int64_t share = (misc->total_units + p.n_clusters - 1) / p.n_clusters;
+  const int64_t share = misc->share;
   Walk wk;
   wk.w0 = share * cl;
   wk.w1 = min(wk.w0 + share, misc->total_units);
@@ -306,8 +315,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t u0 = wk.u + kRowUnits;
     if (first.next(p) && wk.w0 > u0 && wk.w0 - share <= u0) {
       c.q0 = first.q0;
-      c.first = (int)(u0 / share);
-      c.count = (int)((u0 + first.chunks - 1) / share) - c.first + 1;
+      c.first = cl - 1;
+      const int64_t last = u0 + first.chunks - 1 - share * c.first;
+      c.count = (int)ceil_div(last + 1, (int)min(share, (int64_t)INT32_MAX));
       c.m = first.m;
     }
     p.cut[cl] = c;
@@ -346,9 +356,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         };
-        int32_t y = 0, y_next = 0;
-        int valid = 0, valid_next = 0;
-        locate(wk.lo, y, valid);
         // the query's blocks 0-7 go through the ring, on their way to TMEM
 #pragma unroll 1
         for (int pl = 0; pl < kKSlots; ++pl) {
@@ -370,6 +377,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++item;
         sent = 0;
+        int32_t y = 0, y_next = 0;
+        int valid = 0, valid_next = 0;
+        locate(wk.lo, y, valid);
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           // validity words of the chunk, 16 slots (never more than a box) at a time
           uint32_t word = ~0u;
@@ -834,11 +844,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool whole = wk.hi - wk.lo == wk.chunks;
         const float mul = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
         const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
-        // Partials: [column / 4][head][4], so that a warp's stores are whole
-        // lines.  Finished rows: 32 bytes of 32 rows at a time through shared
-        // memory, so that two lanes write a row's piece.
+        // Partials: fp16, scaled by a power of two that brings the largest of
+        // the row's 256 columns here to [1, 2): 11 bits against the 8 of P, and
+        // half the bytes of fp32 (an SM writes about 32 bytes a cycle: a 128-row
+        // fp32 partial took 8600 cycles).  [column / 8][row][8], so that a
+        // warp's stores are whole lines.
+        // Finished rows: 32 bytes of 32 rows at a time through shared memory,
+        // so that two lanes write a row's piece.
         const int pm = p.tp * p.H;  // rows a partial has room for
-        float4* const pout = reinterpret_cast<float4*>(p.part_o + part * pm * kDV) + h;
+        uint4* const pout = p.part_o + part * pm * (kDV / 8) + h;
         uint8_t* const rowp = ostage + lane * 32;
         const int sw = (lane >> 2) & 1;
         const int elt = p.out_bf16 ? 2 : 4;
@@ -855,6 +869,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         };
+        float scale = mul;
+        if (!whole) {
+          float big = 0.f;
+#pragma unroll 1
+          for (int c0 = col0; c0 < col0 + 256; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(lane_addr + c0, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float v = fabsf(__uint_as_float(ov[c]));
+              if (v < INFINITY) big = fmaxf(big, v);
+            }
+          }
+          const int e = max((int)(__float_as_uint(big) >> 23), 1);  // biased exponent, 1 .. 254
+          scale = __uint_as_float((uint32_t)(254 - min(e, 253)) << 23);
+          if (h < wk.m) p.part_sc[(2 * part + (warp >> 2)) * pm + h] = 1.f / scale;  // powers of two: exact
+        }
 #pragma unroll 1
         for (int c0 = col0; c0 < col0 + 256; c0 += 32) {
           uint32_t ov[32];
@@ -862,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld32(lane_addr + c0, ov);
             tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = l == 0.f && whole ? 0u : __float_as_uint(__uint_as_float(ov[c]) * mul);
+            for (int c = 0; c < 32; ++c) ov[c] = l == 0.f && whole ? 0u : __float_as_uint(__uint_as_float(ov[c]) * scale);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
@@ -870,21 +902,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!whole) {
             if (h < wk.m) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
-                pout[(int64_t)(c0 / 4 + c) * pm] =
-                    make_float4(__uint_as_float(ov[4 * c]), __uint_as_float(ov[4 * c + 1]), __uint_as_float(ov[4 * c + 2]),
-                                __uint_as_float(ov[4 * c + 3]));
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 t2 = __floats2half2_rn(__uint_as_float(ov[8 * c + 2 * e]), __uint_as_float(ov[8 * c + 2 * e + 1]));
+                  w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+                }
+                pout[(int64_t)(c0 / 8 + c) * pm] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
             }
           } else if (p.out_bf16) {
-#pragma unroll
+#pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {
+              // (constant register indexes: both halves are spelled out by the select)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 uint32_t w4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 t2 = __floats2bfloat162_rn(__uint_as_float(ov[16 * hf + 8 * c + 2 * e]),
-                                                                   __uint_as_float(ov[16 * hf + 8 * c + 2 * e + 1]));
+                  const uint32_t lo = hf ? ov[16 + 8 * c + 2 * e] : ov[8 * c + 2 * e];
+                  const uint32_t hi = hf ? ov[16 + 8 * c + 2 * e + 1] : ov[8 * c + 2 * e + 1];
+                  const __nv_bfloat162 t2 = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
                   w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
                 }
                 *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
@@ -928,20 +967,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of the cut rows: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// A task is (cut row, 32 heads, 8 / SPLIT column quads); lane = head, and SPLIT
-// warps share a row's partials, their sums meeting in shared memory in a
-// fixed order.
+// A task is (cut tile, 32 rows, 8 / SPLIT groups of eight columns); lane = row.
+// SPLIT warps share a tile's partials, each with the maximum of its own, and
+// the first of them joins their sums in a fixed order: with one long row the
+// partials are many and the rows few (64 partials: 8 loads in flight per
+// thread instead of 64 one behind the other), with many rows it is the other
+// way round.
 constexpr int kCombineWarps = 8;
 constexpr int kMaxClusters = 128;
 
 template <int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
-                             const float4* __restrict__ part_o, int n_clusters, int pm, void* out, int out_bf16, float* lse) {
-  constexpr int kQuads = kCombineWarps / SPLIT;  // column quads per task
+                             const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_clusters, int pm,
+                             void* out, int out_bf16, float* lse) {
+  constexpr int kGroups = kCombineWarps / SPLIT;  // column groups per task
+  constexpr int kFlight = 8;                       // partials a thread has in flight
   __shared__ CutRow s_cut[kMaxClusters];
   __shared__ int s_n;
-  __shared__ float s_sum[kCombineWarps][5][32];
+  __shared__ float s_sum[SPLIT > 1 ? kCombineWarps : 1][10][32];
   grid_dependency_wait();
   allow_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -957,61 +1001,98 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int hgroups = (pm + 31) / 32, per_row = hgroups * (kDV / 4 / kQuads);
+  const int hgroups = (pm + 31) / 32, per_row = hgroups * (kDV / 8 / kGroups);
   const int tasks = s_n * per_row;
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
     const CutRow c = s_cut[task / per_row];
     const int rest = task % per_row;
-    const int h = rest % hgroups * 32 + lane, quad = rest / hgroups * kQuads + warp / SPLIT, sub = warp % SPLIT;
-    // the first partial is its cluster's second, the others are their clusters' first
-    auto part = [&](int i) -> int64_t { return 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0); };
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int h = rest % hgroups * 32 + lane, grp = rest / hgroups * kGroups + warp / SPLIT, sub = warp % SPLIT;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     float M = -INFINITY, l = 0.f;
     if (h < c.m) {
-#pragma unroll 8
-      for (int i = 0; i < c.count; ++i) M = fmaxf(M, __ldg(part_ml + 2 * part(i) * pm + h));
-      const float off = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-      for (int i = sub; i < c.count; i += SPLIT) {
-        const float4 o = __ldg(part_o + (part(i) * (kDV / 4) + quad) * pm + h);
-        const float w = exp2f(__ldg(part_ml + 2 * part(i) * pm + h) - off);
-        l = fmaf(w, __ldg(part_ml + (2 * part(i) + 1) * pm + h), l);
-        a.x = fmaf(w, o.x, a.x);
-        a.y = fmaf(w, o.y, a.y);
-        a.z = fmaf(w, o.z, a.z);
-        a.w = fmaf(w, o.w, a.w);
+      for (int i0 = sub; i0 < c.count; i0 += SPLIT * kFlight) {
+        uint4 o[kFlight];
+        float m[kFlight], li[kFlight], sc[kFlight], top = M;
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const int i = i0 + SPLIT * k;
+          m[k] = -INFINITY;
+          li[k] = sc[k] = 0.f;
+          o[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (i < c.count) {
+            // the first partial is its cluster's second, the others are their clusters' first
+            const int64_t part = 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0);
+            m[k] = __ldg(part_ml + 2 * part * pm + h);
+            li[k] = __ldg(part_ml + (2 * part + 1) * pm + h);
+            sc[k] = __ldg(part_sc + (2 * part + (grp >= kDV / 16 ? 1 : 0)) * pm + h);
+            o[k] = __ldg(part_o + (part * (kDV / 8) + grp) * pm + h);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) top = fmaxf(top, m[k]);
+        const float off = top == -INFINITY ? 0.f : top;
+        const float a = exp2f(M - off);  // 0 at first
+        M = top;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= a;
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const float w = exp2f(m[k] - off), ws = w * sc[k];
+          l = fmaf(w, li[k], l);
+          const uint32_t w4[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+            acc[2 * e] = fmaf(ws, f.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(ws, f.y, acc[2 * e + 1]);
+          }
+        }
       }
     }
     if (SPLIT > 1) {
       __syncthreads();  // the sums of the task before are read
-      s_sum[warp][0][lane] = a.x;
-      s_sum[warp][1][lane] = a.y;
-      s_sum[warp][2][lane] = a.z;
-      s_sum[warp][3][lane] = a.w;
-      s_sum[warp][4][lane] = l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_sum[warp][e][lane] = acc[e];
+      s_sum[warp][8][lane] = l;
+      s_sum[warp][9][lane] = M;
       __syncthreads();
       if (sub != 0) continue;
+      float top = M;
 #pragma unroll
-      for (int u = 1; u < SPLIT; ++u) {
-        a.x += s_sum[warp + u][0][lane];
-        a.y += s_sum[warp + u][1][lane];
-        a.z += s_sum[warp + u][2][lane];
-        a.w += s_sum[warp + u][3][lane];
-        l += s_sum[warp + u][4][lane];
+      for (int u = 1; u < SPLIT; ++u) top = fmaxf(top, s_sum[warp + u][9][lane]);
+      const float off = top == -INFINITY ? 0.f : top;
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < SPLIT; ++u) {
+        const float w = exp2f(s_sum[warp + u][9][lane] - off);
+        l = fmaf(w, s_sum[warp + u][8][lane], l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, s_sum[warp + u][e][lane], acc[e]);
       }
+      M = top;
     }
     if (h >= c.m) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
     const int64_t rh = (int64_t)c.q0 + h;
     if (out_bf16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y), y = __floats2bfloat162_rn(a.z, a.w);
-      reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[quad] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      uint32_t w4[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 t2 = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+        w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+      }
+      reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + rh * kDV)[grp] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
     } else {
-      reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + rh * kDV)[quad] = a;
+      float4* const o4 = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + rh * kDV) + 2 * grp;
+      o4[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      o4[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     }
-    if (quad == 0 && lse) lse[rh] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    if (grp == 0 && lse) lse[rh] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -1051,7 +1132,7 @@ int tokens_per_tile(int T, int H) { return std::max(1, std::min(T, 128 / H)); }
 
 size_t paged_workspace(int T, int H) {
   const size_t n = (size_t)paged_clusters(), m = (size_t)tokens_per_tile(T, H) * H;
-  return n * sizeof(CutRow) + 2 * n * m * 2 * sizeof(float) + 2 * n * m * kDV * sizeof(float);
+  return n * sizeof(CutRow) + 2 * n * m * kDV * sizeof(__half) + 2 * n * m * 4 * sizeof(float);
 }
 
 }  // namespace
@@ -1094,8 +1175,10 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.out_bf16 = out_dtype == DSA_BF16 ? 1 : 0;
   p.lse = lse;
   p.cut = reinterpret_cast<CutRow*>(workspace);
-  p.part_o = reinterpret_cast<float*>(p.cut + n);
-  p.part_ml = p.part_o + (size_t)2 * n * p.tp * H * kDV;
+  const size_t pm = (size_t)p.tp * H;
+  p.part_o = reinterpret_cast<uint4*>(p.cut + n);
+  p.part_ml = reinterpret_cast<float*>(p.part_o + 2 * n * pm * (kDV / 8));
+  p.part_sc = p.part_ml + 2 * n * pm * 2;
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
   p.wait_limit_ns = debug.wait_limit_ns;
@@ -1117,13 +1200,13 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   if (n > 1) {
-    // a few rows are cut into many partials, many rows into two or three
-    const bool few = p.n_rows <= 4;
-    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * ((p.tp * H + 31) / 32) * (kDV / 4) * (few ? 4 : 1) / kCombineWarps;
+    // eight partials and more per row on average: eight warps share them
+    const bool few = p.n_rows <= n / 8;
+    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8) * (few ? 8 : 1) / kCombineWarps;
     const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * kCombineWarps);
-    const auto kernel = few ? paged_mla_combine_kernel<4> : paged_mla_combine_kernel<1>;
-    if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml,
-                   reinterpret_cast<const float4*>(p.part_o), n, p.tp * H, out, p.out_bf16, lse) != cudaSuccess)
+    const auto kernel = few ? paged_mla_combine_kernel<8> : paged_mla_combine_kernel<1>;
+    if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float*)p.part_sc,
+                   (const uint4*)p.part_o, n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;
   }
   return DSA_OK;
