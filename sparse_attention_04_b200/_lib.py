@@ -232,20 +232,19 @@ def decode_step(q_idx, w, k_idx, k_scale, q, kv, offsets, B, max_end_pos, kv_row
 # other here: the library sees pointers only.
 
 def _arg(t, dtype, shape, what, dev, rows=False):
-    """Pointer of a CUDA tensor of this type and shape on `dev`; None gives NULL.
-    rows: a 2-D tensor whose rows may lie further apart than they are long."""
+    """Pointer of a CUDA tensor of this type and shape on device number `dev`;
+    None gives NULL.  rows: a 2-D tensor whose rows may lie further apart than
+    they are long."""
     if t is None:
         return None
-    if t.dtype is not dtype or tuple(t.shape) != shape:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and (t.is_contiguous() or rows):
+        if not rows or t.is_contiguous() or (t.stride(1) == 1 and (t.stride(0) >= shape[1] or shape[0] == 1)):
+            return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
         raise DSAError(1, f"{what} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise DSAError(1, f"{what} is on {t.device}, not on {dev}")
-    if rows:
-        if t.numel() and (t.stride(1) != 1 or (t.stride(0) < shape[1] and shape[0] > 1)):
-            raise DSAError(1, f"the rows of {what} are not contiguous")
-    elif not t.is_contiguous():
-        raise DSAError(1, f"{what} is not contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise DSAError(1, f"{what} is on {t.device}, not on cuda:{dev}")
+    raise DSAError(1, f"the rows of {what} are not contiguous" if rows else f"{what} is not contiguous")
 
 
 def _row_pitch(t):
@@ -253,27 +252,40 @@ def _row_pitch(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+# The current stream's handle by device number: torch.cuda.current_stream()
+# builds a Stream object first, 3.4 us a call against 0.07.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _run_on(dev, stream, fn, what, *args):
-    """fn(*args, stream) on `dev`, whatever device is current."""
-    if stream is not None and stream.device != dev:
-        raise DSAError(1, f"{what}: the stream is on {stream.device}, the tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    """fn(*args, stream) on device number `dev`, whatever device is current."""
+    if stream is not None and stream.device.index != dev:
+        raise DSAError(1, f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
-    _check(rc, what)
+            rc = fn(*args, handle)
+    if rc:
+        raise DSAError(rc, what)
 
 
 def _pages(kv_pages, page_table, what):
-    """(device, B, page_size, n_pages) of a paged cache, checked."""
-    if kv_pages.dim() != 3 or kv_pages.shape[2] != 576 or kv_pages.dtype is not torch.bfloat16:
+    """(device number, B, page_size, n_pages, pool pointer, table pointer, table
+    row pitch, max_pages) of a paged cache, checked."""
+    shape = kv_pages.shape
+    if len(shape) != 3 or shape[2] != 576:
         raise DSAError(1, f"{what}: kv_pages must be bfloat16 [n_pages, page_size, 576]")
-    if not kv_pages.is_cuda:
+    dev = kv_pages.get_device()
+    if dev < 0:
         raise DSAError(1, f"{what}: kv_pages is not on a CUDA device")
-    if page_table.dim() != 2:
+    table = page_table.shape
+    if len(table) != 2:
         raise DSAError(1, f"{what}: page_table must be [B, max_pages]")
-    return kv_pages.device, page_table.shape[0], kv_pages.shape[1], kv_pages.shape[0]
+    return (dev, table[0], shape[1], shape[0], _arg(kv_pages, torch.bfloat16, shape, "kv_pages", dev),
+            _arg(page_table, torch.int32, table, "page_table", dev, rows=True), _row_pitch(page_table), table[1])
 
 
 def _slots(acc, pos, B, dev):
@@ -297,16 +309,15 @@ def _out_code(out, shape, dev):
 def paged_append(kv_new, kv_pages, page_table, lens, acc=None, pos=None, end_pos=None, status=None, stream=None):
     """dsa_paged_append: the newest T tokens' rows kv_new [B,T,576] into each
     sequence's last T slots, acc = 0 and pos = end_pos - T + t beside them."""
-    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_append")
+    dev, B, P, n_pages, kv, table, ld_table, max_pages = _pages(kv_pages, page_table, "paged_append")
     if kv_new.dim() != 3:
         raise DSAError(1, "paged_append: kv_new must be [B, T, 576]")
     T = kv_new.shape[1]
     a, p, ld = _slots(acc, pos, B, dev)
     _run_on(dev, stream, lib.dsa_paged_append, "dsa_paged_append",
-            _arg(kv_new, torch.bfloat16, (B, T, 576), "kv_new", dev), _arg(lens, torch.int32, (B,), "lens", dev),
-            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
-            page_table.shape[1], B, T, P, n_pages, _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
-            a, p, _arg(end_pos, torch.int32, (B,), "end_pos", dev), ld, _arg(status, torch.int32, (1,), "status", dev))
+            _arg(kv_new, torch.bfloat16, (B, T, 576), "kv_new", dev), _arg(lens, torch.int32, (B,), "lens", dev), table,
+            ld_table, max_pages, B, T, P, n_pages, kv, a, p, _arg(end_pos, torch.int32, (B,), "end_pos", dev), ld,
+            _arg(status, torch.int32, (1,), "status", dev))
 
 
 def paged_mla_workspace_size(B, T, H) -> int:
@@ -317,25 +328,23 @@ def paged_mla_workspace_size(B, T, H) -> int:
 def paged_mla(q, kv_pages, page_table, lens, scale, out, lse=None, workspace=None, status=None, stream=None):
     """dsa_paged_mla: attention of q [B,T,H,576] over the whole paged cache
     into out [B,T,H,512] (bf16 or fp32 by out's dtype) and lse [B,T,H]."""
-    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_mla")
+    dev, B, P, n_pages, kv, table, ld_table, max_pages = _pages(kv_pages, page_table, "paged_mla")
     if q.dim() != 4:
         raise DSAError(1, "paged_mla: q must be [B, T, H, 576]")
     T, H = q.shape[1], q.shape[2]
     code, o = _out_code(out, (B, T, H, 512), dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    ws = None if workspace is None else _arg(workspace, workspace.dtype, tuple(workspace.shape), "workspace", dev)
-    _run_on(dev, stream, lib.dsa_paged_mla, "dsa_paged_mla", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev),
-            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
-            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
-            page_table.shape[1], _arg(lens, torch.int32, (B,), "lens", dev), B, T, H, P, n_pages, float(scale), o, code,
-            _arg(lse, torch.float32, (B, T, H), "lse", dev), ws, ws_bytes, _arg(status, torch.int32, (1,), "status", dev))
+    ws = None if workspace is None else _arg(workspace, workspace.dtype, workspace.shape, "workspace", dev)
+    _run_on(dev, stream, lib.dsa_paged_mla, "dsa_paged_mla", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev), kv, table,
+            ld_table, max_pages, _arg(lens, torch.int32, (B,), "lens", dev), B, T, H, P, n_pages, scale, o, code,
+            _arg(lse, torch.float32, (B, T, H), "lse", dev), ws, 0 if ws is None else workspace.nbytes,
+            _arg(status, torch.int32, (1,), "status", dev))
 
 
 def paged_weights(q, kv_pages, page_table, lens, lse, scale, acc, acc_out=None, decay=1.0, status=None, stream=None):
     """dsa_paged_weights: acc_out [B,slots] = decay * acc + the attention
     weight every slot gets from q [B,T,H,576].  acc_out: acc itself unless
     given; acc=None counts as zeros."""
-    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_weights")
+    dev, B, P, n_pages, kv, table, ld_table, max_pages = _pages(kv_pages, page_table, "paged_weights")
     if q.dim() != 4:
         raise DSAError(1, "paged_weights: q must be [B, T, H, 576]")
     T, H = q.shape[1], q.shape[2]
@@ -345,12 +354,9 @@ def paged_weights(q, kv_pages, page_table, lens, lse, scale, acc, acc_out=None, 
         raise DSAError(1, "paged_weights: acc or acc_out is needed")
     o, _, ld = _slots(acc_out, None, B, dev)
     a = o if acc is acc_out else _arg(acc, torch.float32, (B, ld), "acc", dev)
-    _run_on(dev, stream, lib.dsa_paged_weights, "dsa_paged_weights",
-            _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev),
-            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
-            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
-            page_table.shape[1], _arg(lens, torch.int32, (B,), "lens", dev),
-            _arg(lse, torch.float32, (B, T, H), "lse", dev), B, T, H, P, n_pages, float(scale), float(decay), a, o, ld,
+    _run_on(dev, stream, lib.dsa_paged_weights, "dsa_paged_weights", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev), kv,
+            table, ld_table, max_pages, _arg(lens, torch.int32, (B,), "lens", dev),
+            _arg(lse, torch.float32, (B, T, H), "lse", dev), B, T, H, P, n_pages, scale, decay, a, o, ld,
             _arg(status, torch.int32, (1,), "status", dev))
 
 
@@ -359,14 +365,14 @@ def evict_plan(acc, pos, lens, end_pos, budget, recent, new_lens, n_moves, move_
     to `budget` slots (pos and end_pos may be None when recent is 0)."""
     if acc.dim() != 2 or move_dst.dim() != 2:
         raise DSAError(1, "evict_plan: acc must be [B, slots], move_dst and move_src [B, moves]")
-    if not acc.is_cuda:
+    dev, B, moves = acc.get_device(), acc.shape[0], move_dst.shape
+    if dev < 0:
         raise DSAError(1, "evict_plan: acc is not on a CUDA device")
-    dev, B, moves = acc.device, acc.shape[0], tuple(move_dst.shape)
     if moves[0] != B:
         raise DSAError(1, "evict_plan: move_dst and move_src need a row per sequence")
     a, p, ld = _slots(acc, pos, B, dev)
     _run_on(dev, stream, lib.dsa_evict_plan, "dsa_evict_plan", a, p, _arg(lens, torch.int32, (B,), "lens", dev),
-            _arg(end_pos, torch.int32, (B,), "end_pos", dev), B, ld, int(budget), int(recent),
+            _arg(end_pos, torch.int32, (B,), "end_pos", dev), B, ld, budget, recent,
             _arg(new_lens, torch.int32, (B,), "new_lens", dev), _arg(n_moves, torch.int32, (B,), "n_moves", dev),
             _arg(move_dst, torch.int32, moves, "move_dst", dev), _arg(move_src, torch.int32, moves, "move_src", dev),
             moves[1], _arg(status, torch.int32, (1,), "status", dev))
@@ -374,14 +380,12 @@ def evict_plan(acc, pos, lens, end_pos, budget, recent, new_lens, n_moves, move_
 
 def paged_move(kv_pages, page_table, n_moves, move_dst, move_src, acc=None, pos=None, status=None, stream=None):
     """dsa_paged_move: carries an eviction plan out on the cache, acc and pos."""
-    dev, B, P, n_pages = _pages(kv_pages, page_table, "paged_move")
+    dev, B, P, n_pages, kv, table, ld_table, max_pages = _pages(kv_pages, page_table, "paged_move")
     if move_dst.dim() != 2 or move_dst.shape[0] != B:
         raise DSAError(1, "paged_move: move_dst and move_src must be [B, moves]")
-    moves = tuple(move_dst.shape)
+    moves = move_dst.shape
     a, p, ld = _slots(acc, pos, B, dev)
-    _run_on(dev, stream, lib.dsa_paged_move, "dsa_paged_move",
-            _arg(kv_pages, torch.bfloat16, (n_pages, P, 576), "kv_pages", dev),
-            _arg(page_table, torch.int32, tuple(page_table.shape), "page_table", dev, rows=True), _row_pitch(page_table),
-            page_table.shape[1], P, n_pages, _arg(n_moves, torch.int32, (B,), "n_moves", dev),
-            _arg(move_dst, torch.int32, moves, "move_dst", dev), _arg(move_src, torch.int32, moves, "move_src", dev),
-            moves[1], B, a, p, ld, _arg(status, torch.int32, (1,), "status", dev))
+    _run_on(dev, stream, lib.dsa_paged_move, "dsa_paged_move", kv, table, ld_table, max_pages, P, n_pages,
+            _arg(n_moves, torch.int32, (B,), "n_moves", dev), _arg(move_dst, torch.int32, moves, "move_dst", dev),
+            _arg(move_src, torch.int32, moves, "move_src", dev), moves[1], B, a, p, ld,
+            _arg(status, torch.int32, (1,), "status", dev))
