@@ -28,10 +28,10 @@ constexpr int kBins = 2048;
 constexpr int kMaxCS = 8;
 constexpr int kSmemMax = 227 * 1024;
 
-struct PlanSmem {
+struct alignas(16) PlanSmem {
   uint32_t hist[3][kBins];  // one per pass: no CTA clears what another still reads
   uint32_t tot[kBins];      // cluster-wide counts of the current pass
-  uint32_t warp_tot[kWarps];
+  alignas(16) uint64_t warp_tot[32];
   uint32_t cnt[2];          // this CTA's free slots below n, survivors from n on
   uint32_t base[2];         // those of the CTAs before it
   uint32_t total;           // moves of the sequence
@@ -61,22 +61,23 @@ __device__ __forceinline__ uint32_t slot_key(float a, bool kept_always) {
 }
 
 // Exclusive scan over the block of one value per thread; *total is the sum.
-__device__ __forceinline__ uint32_t scan_excl(uint32_t v, PlanSmem& sm, uint32_t* total) {
+__device__ __noinline__ uint64_t scan_excl(uint64_t v, PlanSmem& sm, uint64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t inc = v;
+  uint64_t* const warp_tot = sm.warp_tot;
+  uint64_t inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    const uint64_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
   __syncthreads();  // warp_tot may still be read from the scan before
-  if (lane == 31) sm.warp_tot[warp] = inc;
+  if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
-  const uint32_t w = sm.warp_tot[lane];
-  uint32_t winc = w;
+  const uint64_t w = lane < kWarps ? warp_tot[lane] : 0ull;
+  uint64_t winc = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xffffffffu, winc, o);
+    const uint64_t u = __shfl_up_sync(0xffffffffu, winc, o);
     if (lane >= o) winc += u;
   }
   *total = __shfl_sync(0xffffffffu, winc, 31);
@@ -122,28 +123,70 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   const int32_t* const pos = a.recent > 0 ? a.pos + (int64_t)b * a.ld + s_lo : nullptr;
   const int64_t protect_from = a.recent > 0 ? (int64_t)a.end_pos[b] - a.recent : 0;
   auto make_key = [&](int i) { return slot_key(acc[i], pos && pos[i] >= protect_from); };
-  auto key_of = [&](int i) { return i < key_cap ? keys[i] : make_key(i); };
 
   for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
   __syncthreads();
-  // ---- keys, and the histogram of their top 11 bits
-  auto count = [&](uint32_t* hist, uint32_t bin, bool on) {
-    // a warp of equal keys (fresh slots, say) adds once
-    const uint32_t mask = __ballot_sync(0xffffffffu, on);
-    if (mask == 0) return;
-    const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(mask) - 1);
-    if (__all_sync(0xffffffffu, !on || bin == first)) {
-      if (lane == 0) atomicAdd(&hist[first], (uint32_t)__popc(mask));
-    } else if (on) {
-      atomicAdd(&hist[bin], 1u);
+  // Adds four keys per lane to a histogram.  A warp whose keys are all alike
+  // (fresh slots, say) adds once; otherwise the few lanes that share a bin are
+  // served one after the other, which costs less than sorting them out.
+  auto count4 = [&](uint32_t* hist, const uint32_t (&bin)[4], const bool (&on)[4]) {
+    const uint32_t first = __shfl_sync(0xffffffffu, bin[0], 0);
+    if (__all_sync(0xffffffffu, on[0] && on[1] && on[2] && on[3] && bin[0] == first && bin[1] == first && bin[2] == first &&
+                                    bin[3] == first)) {
+      if (lane == 0) atomicAdd(&hist[first], 128u);
+      return;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (on[e]) atomicAdd(&hist[bin[e]], 1u);
   };
-  for (int i0 = 0; i0 < m; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t key = i < m ? make_key(i) : 0u;
-    if (i < m && i < key_cap) keys[i] = key;
-    count(sm.hist[0], key >> 21, i < m);
+  // ---- keys, four slots per thread at a time and kFlight such groups in
+  // flight, and the histogram of their top 11 bits
+  constexpr int kFlight = 2;
+  const int m4 = (m + 3) / 4;
+  for (int g0 = 0; g0 < m4; g0 += kFlight * kThreads) {
+    float4 av[kFlight];
+    int4 pv[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int g = g0 + k * kThreads + threadIdx.x;
+      av[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      pv[k] = make_int4(INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN);
+      if (4 * g < m) {  // (whole groups: the rows' pitch is a multiple of 4)
+        av[k] = __ldcs(reinterpret_cast<const float4*>(acc) + g);
+        if (pos) pv[k] = __ldcs(reinterpret_cast<const int4*>(pos) + g);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int g = g0 + k * kThreads + threadIdx.x;
+      if (__all_sync(0xffffffffu, 4 * g >= m)) break;
+      const float a4[4] = {av[k].x, av[k].y, av[k].z, av[k].w};
+      const int p4[4] = {pv[k].x, pv[k].y, pv[k].z, pv[k].w};
+      uint32_t key[4], bin[4];
+      bool on[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        key[e] = slot_key(a4[e], pos && p4[e] >= protect_from);
+        bin[e] = key[e] >> 21;
+        on[e] = 4 * g + e < m;
+      }
+      count4(sm.hist[0], bin, on);
+      if (4 * g < key_cap) *reinterpret_cast<uint4*>(keys + 4 * g) = make_uint4(key[0], key[1], key[2], key[3]);
+    }
   }
+  __syncthreads();
+  // keys of the slots 4g .. 4g + 3 (those at or behind m are of no meaning)
+  auto keys_of = [&](int g) -> uint4 {
+    if (4 * g < key_cap) return *reinterpret_cast<const uint4*>(keys + 4 * g);
+    uint4 k = make_uint4(0u, 0u, 0u, 0u);
+    if (4 * g < m) k.x = make_key(4 * g);
+    if (4 * g + 1 < m) k.y = make_key(4 * g + 1);
+    if (4 * g + 2 < m) k.z = make_key(4 * g + 2);
+    if (4 * g + 3 < m) k.w = make_key(4 * g + 3);
+    return k;
+  };
+  auto key_of = [&](int i) { return i < key_cap ? keys[i] : make_key(i); };
   // ---- three digit passes: tau, and how many keys equal to it stay
   uint32_t prefix = 0, remaining = (uint32_t)n;
 #pragma unroll 1
@@ -152,10 +195,18 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     const int bins = pass == 2 ? 1024 : 2048;
     if (pass > 0) {
       const int pshift = pass == 1 ? 21 : 10;
-      for (int i0 = 0; i0 < m; i0 += kThreads) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t key = i < m ? key_of(i) : 0u;
-        count(sm.hist[pass], (key >> shift) & (uint32_t)(bins - 1), i < m && (key >> pshift) == (prefix >> pshift));
+      for (int g0 = 0; g0 < m4; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        const uint4 k4 = g < m4 ? keys_of(g) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+        bool on[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) on[e] = 4 * g + e < m && (key[e] >> pshift) == (prefix >> pshift);
+        if (!__any_sync(0xffffffffu, on[0] || on[1] || on[2] || on[3])) continue;  // mostly: few keys share a prefix
+        uint32_t bin[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bin[e] = (key[e] >> shift) & (uint32_t)(bins - 1);
+        count4(sm.hist[pass], bin, on);
       }
     }
     cluster.sync();
@@ -166,15 +217,26 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     }
     __syncthreads();
     // the bin, from the top, that holds the remaining-th largest key: thread
-    // t takes the bins bins-1-2t and bins-2-2t
-    const int hi = bins - 1 - 2 * (int)threadIdx.x;
-    const uint32_t c0 = hi > 0 ? sm.tot[hi] : 0u, c1 = hi > 0 ? sm.tot[hi - 1] : 0u;
-    uint32_t all;
-    const uint32_t above = scan_excl(c0 + c1, sm, &all);
-    if (above < remaining && remaining <= above + c0 + c1) {
-      const bool second = remaining > above + c0;
-      sm.digit = (uint32_t)(second ? hi - 1 : hi);
-      sm.remaining = remaining - above - (second ? c0 : 0u);
+    // t takes the kPer bins from bins-1 - kPer t downwards
+    constexpr int kPer = kBins / kThreads;
+    const int hi = bins - 1 - kPer * (int)threadIdx.x;
+    uint32_t c[kPer], mine = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      c[e] = hi - e >= 0 ? sm.tot[hi - e] : 0u;
+      mine += c[e];
+    }
+    uint64_t all;
+    uint32_t above = (uint32_t)scan_excl(mine, sm, &all);
+    if (above < remaining && remaining <= above + mine) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (above < remaining && remaining <= above + c[e]) {
+          sm.digit = (uint32_t)(hi - e);
+          sm.remaining = remaining - above;
+        }
+        above += c[e];
+      }
     }
     __syncthreads();
     prefix |= sm.digit << shift;
@@ -194,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   const int wpt = (words + kThreads - 1) / kThreads;
   for (int w = warp; w < words; w += kWarps) {
     const int i = 32 * w + lane;
-    const uint32_t key = i < m ? key_of(i) : 0u;
+    const uint32_t key = m <= key_cap ? keys[i] : i < m ? key_of(i) : 0u;  // (keys holds whole words)
     const uint32_t up = __ballot_sync(0xffffffffu, i < m && key > tau);
     const uint32_t eq = __ballot_sync(0xffffffffu, i < m && key == tau);
     if (lane == 0) {
@@ -204,9 +266,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   }
   __syncthreads();
   const int w_lo = min((int)threadIdx.x * wpt, words), w_hi = min(w_lo + wpt, words);
-  uint32_t eqs = 0, unused;
-  for (int w = w_lo; w < w_hi; ++w) eqs += __popc(bitmap[2 * w + 1]);
-  uint32_t eq_rank = sm.eq_before + scan_excl(eqs, sm, &unused);
+  uint32_t eq_rank = 0;
+  const bool all_eq = sm.tot[tau & 1023u] == need_eq;  // every key equal to tau stays: no ranks are needed
+  if (!all_eq) {
+    uint32_t eqs = 0;
+    uint64_t unused;
+    for (int w = w_lo; w < w_hi; ++w) eqs += __popc(bitmap[2 * w + 1]);
+    eq_rank = sm.eq_before + (uint32_t)scan_excl(eqs, sm, &unused);
+  }
   // slots of word w below n
   auto below = [&](int w) -> uint32_t {
     const int k = n - (s_lo + 32 * w);
@@ -216,6 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   uint32_t free_n = 0, surv_n = 0;
   for (int w = w_lo; w < w_hi; ++w) {
     uint32_t keep = bitmap[2 * w], eq = bitmap[2 * w + 1];
+    if (all_eq) {
+      keep |= eq;
+      eq = 0;
+    }
     while (eq && eq_rank < need_eq) {
       const uint32_t low = eq & (0u - eq);
       keep |= low;
@@ -226,9 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     free_n += __popc(~keep & below(w) & held(w));
     surv_n += __popc(keep & ~below(w));
   }
-  uint32_t free_all, surv_all;
-  uint32_t fr = scan_excl(free_n, sm, &free_all);
-  uint32_t sr = scan_excl(surv_n, sm, &surv_all);
+  uint64_t both_all;
+  const uint64_t both = scan_excl((uint64_t)surv_n << 32 | free_n, sm, &both_all);
+  uint32_t fr = (uint32_t)both, sr = (uint32_t)(both >> 32);
+  const uint32_t free_all = (uint32_t)both_all, surv_all = (uint32_t)(both_all >> 32);
   if (threadIdx.x == 0) {
     sm.cnt[0] = free_all;
     sm.cnt[1] = surv_all;
@@ -257,12 +329,33 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     pad_lists(0);
     return;
   }
+  // A word below n holds free slots, one from n on survivors; the word that n
+  // cuts holds both, and its survivors are the first of all.  So one mask and
+  // one rank per word say what is to be written, and the thread that owns the
+  // cut word writes its survivors itself.
   fr += sm.base[0];
   sr += sm.base[1];
   for (int w = w_lo; w < w_hi; ++w) {
-    uint32_t f = ~bitmap[2 * w] & below(w) & held(w), s = bitmap[2 * w] & ~below(w);
-    for (; f; f &= f - 1) dst[fr++] = s_lo + 32 * w + __ffs((int)f) - 1;
-    for (; s; s &= s - 1) src[sr++] = s_lo + 32 * w + __ffs((int)s) - 1;
+    const uint32_t keep = bitmap[2 * w], f = ~keep & below(w) & held(w), sv = keep & ~below(w);
+    const bool low = s_lo + 32 * w < n;
+    bitmap[2 * w] = low ? f : sv;
+    bitmap[2 * w + 1] = low ? fr : sr;
+    fr += __popc(f);
+    sr += __popc(sv);
+    if (low) {
+      int at = 0;
+      for (uint32_t x = sv; x; x &= x - 1) src[at++] = s_lo + 32 * w + __ffs((int)x) - 1;
+    }
+  }
+  __syncthreads();
+  // a warp writes a word's entries side by side
+  const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll 2
+  for (int w = warp; w < words; w += kWarps) {
+    const uint2 v = *reinterpret_cast<const uint2*>(bitmap + 2 * w);
+    const int slot = s_lo + 32 * w + lane;
+    int32_t* const list = s_lo + 32 * w < n ? dst : src;
+    if ((v.x >> lane) & 1u) list[v.y + __popc(v.x & lower)] = slot;
   }
   if (rank == 0 && threadIdx.x == 0) {
     a.new_lens[b] = n;
@@ -287,12 +380,15 @@ extern "C" int dsa_evict_plan(const float* acc, const int32_t* pos, const int32_
   if (recent > 0 && (!pos || !end_pos)) return DSA_ERR_INVALID_ARG;
   if (int rc = check_slots(acc, pos, ld_slots)) return rc;
   if (ld_slots > DSA_MAX_PLAN_SLOTS) return DSA_ERR_UNSUPPORTED;
-  // CTAs per sequence: one per 8192 slots, up to eight (a portable cluster)
+  // CTAs per sequence: one per 8192 slots, up to eight (a portable cluster);
+  // fewer while the sequences make more than one wave of CTAs and the keys
+  // still fit on chip (32 sequences of 131072 slots: 4 instead of 8).
   int cs = 1;
   while (cs < kMaxCS && ld_slots > (int64_t)8192 * cs) cs *= 2;
+  while (cs > 1 && (int64_t)B * cs > device_info().sm_count && ld_slots <= (int64_t)40960 * (cs / 2)) cs /= 2;
   const int64_t slice = ((ld_slots + cs - 1) / cs + 127) / 128 * 128;
   const int64_t fixed = (int64_t)sizeof(PlanSmem) + 8 * ((slice + 31) / 32);
-  const int key_cap = (int)std::min<int64_t>(slice, (kSmemMax - fixed) / 4);
+  const int key_cap = (int)std::min<int64_t>(slice, (kSmemMax - fixed) / 16 * 4);
   const int64_t smem = fixed + 4 * (int64_t)key_cap;
   static PerDeviceOnce attr;
   if (attr.run([] {
