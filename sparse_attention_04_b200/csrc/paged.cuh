@@ -37,6 +37,27 @@ __device__ __forceinline__ int32_t checked_len(int32_t len, int64_t cap, bool& b
   return bad ? 0 : len;
 }
 
+// ceil(a / b); the quotient in 32 bits where they hold it (a 64-bit division
+// takes a few hundred cycles).
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int b) {
+  const int64_t n = a + b - 1;
+  return n < ((int64_t)1 << 31) ? (int64_t)((uint32_t)n / (uint32_t)b) : n / b;
+}
+
+// NBOX boxes of BOX rows, NBLK column blocks each, into blocks of BYTES.
+// Spelled out: an issue then takes about 16 cycles, in a loop over the boxes 45.
+template <int BOX, int NBOX, int NBLK, int BYTES>
+__device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap* tm, int x0, const int32_t* ys, uint32_t full) {
+  int32_t y[NBOX];
+#pragma unroll
+  for (int i = 0; i < NBOX; ++i) y[i] = ys[i];
+#pragma unroll
+  for (int i = 0; i < NBOX; ++i)
+#pragma unroll
+    for (int blk = 0; blk < NBLK; ++blk)
+      tma_load_2d(dst + blk * BYTES + i * BOX * 128, tm, x0 + 64 * blk, y[i], full);
+}
+
 inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool is_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 

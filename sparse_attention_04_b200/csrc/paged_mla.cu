@@ -153,13 +153,6 @@ __device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool&
 }
 __device__ __forceinline__ int64_t n_chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
 
-// ceil(a / b); the quotient in 32 bits where they hold it (a 64-bit division
-// takes a few hundred cycles).
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int b) {
-  const int64_t n = a + b - 1;
-  return n < ((int64_t)1 << 31) ? (int64_t)((uint32_t)n / (uint32_t)b) : n / b;
-}
-
 // One after the other, the parts of tiles that fall to this cluster.  Every
 // role of both CTAs walks the same list.
 struct Walk {
@@ -192,20 +185,6 @@ struct Walk {
     return false;
   }
 };
-
-// NBOX boxes of BOX rows, NBLK column blocks each, into blocks of BYTES.
-// Spelled out: an issue then takes about 16 cycles, in a loop over the boxes 45.
-template <int BOX, int NBOX, int NBLK, int BYTES>
-__device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap* tm, int x0, const int32_t* ys, uint32_t full) {
-  int32_t y[NBOX];
-#pragma unroll
-  for (int i = 0; i < NBOX; ++i) y[i] = ys[i];
-#pragma unroll
-  for (int i = 0; i < NBOX; ++i)
-#pragma unroll
-    for (int blk = 0; blk < NBLK; ++blk)
-      tma_load_2d(dst + blk * BYTES + i * BOX * 128, tm, x0 + 64 * blk, y[i], full);
-}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

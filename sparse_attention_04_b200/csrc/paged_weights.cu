@@ -5,16 +5,21 @@
 // The cache is read once (1152 bytes a slot), against 2 * 576 flops and one
 // exponential per slot and head: HBM bounds it up to 128 (token, head) rows.
 //
-// S^T = K.Q^T, the slots as the M = 128 rows of the product: a thread of the
-// epilogue then owns one slot (TMEM lane) and sums over heads in its own
-// registers, in a fixed order, in fp32.  The query rows of a sequence, up to
-// 128 (t, h) pairs at a time, stay in shared memory as the B operand; a
-// chunk's rows stream through a ring of 128-row x 64-column blocks, as many
-// places as fit beside the query.  Every CTA takes an equal, contiguous part of
-// the list of all sequences' 128-slot chunks.
+// S = Q.K^T with the (token, head) rows of a sequence, up to 128 at a time, as
+// the product's M: all but one of the query's 64-column blocks stay in TMEM as
+// the A operand, which leaves shared memory to the ring that the cache streams
+// through, four places of three 128-row x 64-column blocks (192 KB: HBM answers
+// in about 2 us under load, so an SM has to keep 90 KB and more in flight.
+// With the query in shared memory as the B operand, 80 KB of ring were left:
+// 140 us against 112 for 16 ragged sequences of 560 K slots in all).
+// A thread of the epilogue owns a query row (TMEM lane) and half of a chunk's
+// slots; the sums over rows run across lanes (a butterfly that halves the
+// columns as it halves the rows) and then across the four warps of a half, in
+// fp32 and in a fixed order.  Every CTA takes an equal, contiguous part of the
+// list of all sequences' 128-slot chunks.
 //
-// Roles: warps 0-3 epilogue, warp 4 loader, warp 5 TMEM allocator and MMA
-// issuer.  S^T has two TMEM buffers, so that the exponentials of a chunk run
+// Roles: warps 0-7 epilogue, warp 8 loader, warp 9 TMEM allocator and MMA
+// issuer.  S has two TMEM buffers, so that the exponentials of a chunk run
 // beside the products of the next.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -27,35 +32,38 @@
 namespace dsa {
 namespace {
 
-constexpr int kChunk = 128;                  // slots per chunk: the product's M
+constexpr int kChunk = 128;                  // slots per chunk: the product's N
 constexpr int kKB = kDQK / 64;               // 64-column blocks of a row: 9
-constexpr int kBlockBytes = kChunk * 128;    // one block of a chunk
-constexpr int kMaxCols = 128;                // (t, h) rows per query tile: the product's N
-constexpr int kMaxPlaces = 12;
-constexpr int kThreads = 192;
-constexpr int kLoadWarp = 4, kMmaWarp = 5;
-constexpr int kSmemTotal = 232448 - 1024;    // behind the 1024-byte alignment
-enum Bar : int { kQFull = 0, kQFree, kKFull, kKEmpty = kKFull + kMaxPlaces, kSFull = kKEmpty + kMaxPlaces, kSEmpty = kSFull + 2, kDrain = kSEmpty + 2, kNumBar };
+constexpr int kBlockBytes = kChunk * 128;    // one block of a chunk, or of a query tile
+constexpr int kRows = 128;                   // (token, head) rows per query tile: the product's M
+constexpr int kPlaceBlocks = 3;
+constexpr int kPlaceBytes = kPlaceBlocks * kBlockBytes;
+constexpr int kPlaces = 4;
+constexpr int kPerChunk = kKB / kPlaceBlocks;  // places a chunk, or a query tile, goes through
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kTmemS = 256;             // query blocks 0-7 in [0, 256), S buffers at 256 and 384
+constexpr uint32_t kIdesc = idesc_bf16(kRows, kChunk);
+enum Bar : int { kQFull = 0, kQFree, kKFull, kKEmpty = kKFull + kPlaces, kSFull = kKEmpty + kPlaces, kSEmpty = kSFull + 2, kDrain = kSEmpty + 2, kNumBar };
 struct Misc {
   uint64_t bars[kNumBar];
-  alignas(16) float lse2[2][kMaxCols];  // lse * log2(e) per column, by query tile parity; +inf where nothing is to be added
-  int32_t y[8];             // row coordinates of a chunk's boxes
+  alignas(16) int32_t y[8];  // row coordinates of a chunk's boxes
+  float part[2][4][kChunk];  // sums over 32 rows each, by chunk parity
   int tmem_base, abort, first_seq, pad;
-  int64_t first_unit, total_units;
+  int64_t first_unit, total_units, share;
   int64_t warp_sum[kThreads / 32];
 };
-constexpr int kMiscBytes = (int)((sizeof(Misc) + 1023) / 1024 * 1024);
-constexpr int kRingOff = kMiscBytes;         // the ring, then the query's blocks
-static_assert(offsetof(Misc, lse2) % 16 == 0 && offsetof(Misc, bars) == 0, "alignment");
-static_assert(kSmemTotal - kMiscBytes - kKB * kMaxCols * 128 >= 4 * kBlockBytes, "four places beside the largest query tile");
+constexpr int kQ8Off = (int)((sizeof(Misc) + 1023) / 1024 * 1024);
+constexpr int kRingOff = kQ8Off + kBlockBytes;
+constexpr int kSmemBytes = kRingOff + kPlaces * kPlaceBytes + 1024;
+static_assert(kSmemBytes <= 232448 && offsetof(Misc, bars) == 0, "shared memory");
 
 struct PagedWeightsParams {
   PagePool pool;
   const int32_t* lens;
   const float* lse;
   int B, T, H;
-  int cols;     // (t, h) rows per query tile, a multiple of 16
-  int places;   // ring places
   int box;      // rows per TMA box
   float scale_log2, decay;
   const float* acc;
@@ -104,18 +112,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + 8u * (uint32_t)i; };
   volatile int* abort = &misc->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t q_off = sbase + kRingOff + p.places * kBlockBytes;
-  const int q_block = p.cols * 128;  // one 64-column block of a query tile
 
   if (threadIdx.x == 0) misc->abort = 0;
   if (warp == kMmaWarp) {
     if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
-      for (int i = 0; i < kNumBar; ++i) mbar_init(bar(i), i >= kSEmpty && i < kSEmpty + 2 ? 4 : 1);
+      for (int i = 0; i < kNumBar; ++i) mbar_init(bar(i), i >= kSEmpty && i < kSEmpty + 2 ? kEpiWarps : 1);
       fence_mbar_init();
     }
     __syncwarp();
-    tmem_alloc(sbase + (uint32_t)offsetof(Misc, tmem_base), 2 * kMaxCols);
+    tmem_alloc(sbase + (uint32_t)offsetof(Misc, tmem_base), 512);
     tmem_relinquish();
   }
   grid_dependency_wait();  // everything may come from the previous kernel
@@ -144,9 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) before += v;
       total += v;
     }
-    const int64_t w0 = (total + gridDim.x - 1) / gridDim.x * blockIdx.x;
+    const int64_t share = ceil_div(total, (int)gridDim.x), w0 = share * blockIdx.x;
     if (threadIdx.x == 0) {
       misc->total_units = total;
+      misc->share = share;
       if (w0 >= total) misc->first_seq = p.B;
     }
     if (before <= w0 && w0 < before + mine) {
@@ -168,29 +176,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
   Walk wk;
-  const int64_t share = (misc->total_units + gridDim.x - 1) / gridDim.x;
+  const int64_t share = misc->share;
   wk.w0 = share * blockIdx.x;
   wk.w1 = min(wk.w0 + share, misc->total_units);
   wk.b = misc->first_seq;
   wk.n_seq = p.B;
   wk.u = wk.b < p.B ? misc->first_unit : 0;
-  const int th = p.T * p.H, n_tiles = (th + p.cols - 1) / p.cols;
+  const int th = p.T * p.H, n_tiles = (th + kRows - 1) / kRows;
 
   if (warp == kLoadWarp) {
     const uint32_t on = elect_one();
     const int nbox = kChunk / p.box;
     const int32_t pool_rows = (int32_t)(p.pool.n_pages * p.pool.page_size);
-    uint32_t tiles = 0, fills = 0;  // query tiles and blocks so far
-    uint32_t place = 0, round = 0;
+    uint32_t tiles = 0, fills = 0;  // query tiles and ring places filled so far
     bool ok = true;
+    auto place_free = [&]() {
+      return warp_wait(bar(kKEmpty + fills % kPlaces), ((fills / kPlaces) & 1) ^ 1, abort, p.wait_limit_ns);
+    };
     while (ok && wk.next(p)) {
       for (int qt = 0; ok && qt < n_tiles; ++qt, ++tiles) {
-        // the query tile, once the products with the one before are complete
-        if (tiles > 0 && !(ok = warp_wait(bar(kQFree), (tiles - 1) & 1, abort, p.wait_limit_ns))) break;
-        if (on) {
-          mbar_arrive_expect_tx(bar(kQFull), kKB * q_block);
+        const int yq = wk.seq * th + qt * kRows;
+        // blocks 0-7 of the query tile go through the ring, on their way to TMEM
 #pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) tma_load_3d(q_off + kb * q_block, &tm_q, kb * 64, qt * p.cols, wk.seq, bar(kQFull));
+        for (int pl = 0; pl < kPerChunk; ++pl) {
+          if (!(ok = place_free())) break;
+          if (on) {
+            const uint32_t place = fills % kPlaces, full = bar(kKFull + place);
+            const int kb0 = kPlaceBlocks * pl, kb1 = min(kb0 + kPlaceBlocks, kKB - 1);
+            mbar_arrive_expect_tx(full, (kb1 - kb0) * kBlockBytes);
+            for (int kb = kb0; kb < kb1; ++kb)
+              tma_load_2d(sbase + kRingOff + place * kPlaceBytes + (kb - kb0) * kBlockBytes, &tm_q, kb * 64, yq, full);
+          }
+          __syncwarp();
+          ++fills;
+        }
+        // block 8, once the products with the tile before are complete
+        if (!ok || (tiles > 0 && !(ok = warp_wait(bar(kQFree), (tiles - 1) & 1, abort, p.wait_limit_ns)))) break;
+        if (on) {
+          mbar_arrive_expect_tx(bar(kQFull), kBlockBytes);
+          tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, yq, bar(kQFull));
         }
         __syncwarp();
         for (int i = wk.lo; ok && i < wk.hi; ++i) {
@@ -204,69 +228,92 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < 8) misc->y[lane] = y;
           __syncwarp();
 #pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) {
-            if (!(ok = warp_wait(bar(kKEmpty + place), (round & 1) ^ 1, abort, p.wait_limit_ns))) break;
+          for (int pl = 0; pl < kPerChunk; ++pl) {
+            if (!(ok = place_free())) break;
             if (on) {
-              const uint32_t full = bar(kKFull + place);
-              uint32_t dst = sbase + kRingOff + place * kBlockBytes;
-              mbar_arrive_expect_tx(full, kBlockBytes);
-#pragma unroll 1
-              for (int bx = 0; bx < nbox; bx += 2, dst += 2 * p.box * 128) {
-                tma_load_2d(dst, &tm_k, kb * 64, misc->y[bx], full);
-                tma_load_2d(dst + p.box * 128, &tm_k, kb * 64, misc->y[bx + 1], full);
-              }
+              const uint32_t place = fills % kPlaces, full = bar(kKFull + place), dst = sbase + kRingOff + place * kPlaceBytes;
+              const int x0 = kPlaceBlocks * pl * 64;
+              mbar_arrive_expect_tx(full, kPlaceBytes);
+              if (p.box == 64) load_boxes<64, 2, kPlaceBlocks, kBlockBytes>(dst, &tm_k, x0, misc->y, full);
+              else if (p.box == 32) load_boxes<32, 4, kPlaceBlocks, kBlockBytes>(dst, &tm_k, x0, misc->y, full);
+              else load_boxes<16, 8, kPlaceBlocks, kBlockBytes>(dst, &tm_k, x0, misc->y, full);
             }
             __syncwarp();
             ++fills;
-            if (++place == (uint32_t)p.places) {
-              place = 0;
-              ++round;
-            }
           }
-          __syncwarp();  // the coordinates are read before the next chunk's are written
         }
       }
     }
     if (*abort) {
       // the loads in flight must land before the CTA exits (10 ms at most each)
       volatile int never = 0;
-      for (uint32_t k = fills > (uint32_t)p.places ? fills - p.places : 0; k < fills; ++k)
-        mbar_wait(bar(kKFull + k % p.places), (k / p.places) & 1, &never, 10000000ull);
+      for (uint32_t k = fills > (uint32_t)kPlaces ? fills - kPlaces : 0; k < fills; ++k)
+        mbar_wait(bar(kKFull + k % kPlaces), (k / kPlaces) & 1, &never, 10000000ull);
       mbar_wait(bar(kQFull), tiles & 1, &never, 10000000ull);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t on = elect_one();
     const uint64_t k0 = smem_desc(sbase + kRingOff, 16, 1024, kSwizzle128B);
-    const uint64_t q0 = smem_desc(q_off, 16, 1024, kSwizzle128B);
-    const uint32_t idesc = idesc_bf16(kChunk, p.cols);
+    const uint64_t q8 = smem_desc(sbase + kQ8Off, 16, 1024, kSwizzle128B);
     auto wait = [&](int which, uint32_t parity) {
       const bool there = warp_wait(bar(which), parity, abort, p.wait_limit_ns);
       tc_fence_after();
       return there;
     };
-    uint32_t tiles = 0, g = 0, place = 0, round = 0;
+    uint32_t tiles = 0, g = 0, fills = 0;
     bool ok = true;
     while (ok && wk.next(p)) {
       for (int qt = 0; ok && qt < n_tiles; ++qt, ++tiles) {
-        if (!(ok = wait(kQFull, tiles & 1))) break;
+        // the query tile into TMEM, once no product reads the one before
+        if (tiles > 0 && !(ok = wait(kQFree, (tiles - 1) & 1))) break;
+#pragma unroll 1
+        for (int pl = 0; pl < kPerChunk; ++pl, ++fills) {
+          const uint32_t place = fills % kPlaces;
+          if (!(ok = wait(kKFull + place, (fills / kPlaces) & 1))) break;
+          if (on) {
+            const uint64_t src = k0 + (uint64_t)((place * kPlaceBytes) >> 4);
+            for (int kb = kPlaceBlocks * pl; kb < min(kPlaceBlocks * (pl + 1), kKB - 1); ++kb)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tmem_cp_128x32b(tmem + kb * 32 + ks * 8,
+                                src + (uint64_t)(((kb - kPlaceBlocks * pl) * kBlockBytes) >> 4) + (uint64_t)ks * 2);
+            tc_commit(bar(kKEmpty + place));
+          }
+          __syncwarp();
+        }
+        if (!ok || !(ok = wait(kQFull, tiles & 1))) break;
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(kSEmpty + sb, ((g - 2) >> 1) & 1))) break;
-          const uint32_t d = tmem + kMaxCols * sb;
+          const uint32_t d = tmem + kTmemS + kChunk * sb;
 #pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) {
-            if (!(ok = wait(kKFull + place, round & 1))) break;
-            const uint64_t ad = k0 + (uint64_t)((place * kBlockBytes) >> 4), bd = q0 + (uint64_t)((kb * q_block) >> 4);
+          for (int pl = 0; pl < kPerChunk - 1; ++pl, ++fills) {
+            const uint32_t place = fills % kPlaces;
+            if (!(ok = wait(kKFull + place, (fills / kPlaces) & 1))) break;
+            const uint64_t bs = k0 + (uint64_t)((place * kPlaceBytes) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_f16_ss_if(on, d, ad + (uint64_t)ks * 2, bd + (uint64_t)ks * 2, idesc, (kb | ks) ? 1u : 0u);
-            if (on) tc_commit(bar(kKEmpty + place));
-            if (++place == (uint32_t)p.places) {
-              place = 0;
-              ++round;
+            for (int u = 0; u < 4 * kPlaceBlocks; ++u) {
+              const int kb = kPlaceBlocks * pl + u / 4, ks = u % 4;
+              mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bs + (uint64_t)(((u / 4) * kBlockBytes) >> 4) + (uint64_t)ks * 2,
+                            kIdesc, (kb | ks) ? 1u : 0u);
             }
+            if (on) tc_commit(bar(kKEmpty + place));
           }
-          if (ok && on) tc_commit(bar(kSFull + sb));
+          const uint32_t place = fills % kPlaces;
+          if (!ok || !(ok = wait(kKFull + place, (fills / kPlaces) & 1))) break;
+          ++fills;
+          const uint64_t bs = k0 + (uint64_t)((place * kPlaceBytes) >> 4);
+#pragma unroll
+          for (int u = 0; u < 4 * kPlaceBlocks; ++u) {
+            const int kb = kKB - kPlaceBlocks + u / 4, ks = u % 4;
+            const uint64_t bd = bs + (uint64_t)(((u / 4) * kBlockBytes) >> 4) + (uint64_t)ks * 2;
+            if (kb < kKB - 1) mma_f16_ts_if(on, d, tmem + kb * 32 + ks * 8, bd, kIdesc, 1u);
+            else mma_f16_ss_if(on, d, q8 + (uint64_t)ks * 2, bd, kIdesc, 1u);
+          }
+          if (on) {
+            tc_commit(bar(kKEmpty + place));
+            tc_commit(bar(kSFull + sb));
+          }
         }
         if (ok && on) tc_commit(bar(kQFree));
       }
@@ -277,66 +324,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bar(kDrain), 0, &never, 10000000ull);
     }
   } else {
-    // ---- epilogue: thread = slot of the chunk
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    uint32_t tiles = 0, g = 0;
-    bool ok = true, leave = false;
-    while (!leave && wk.next(p)) {
-      for (int qt = 0; qt < n_tiles; ++qt, ++tiles) {
-        float* const lse2 = misc->lse2[tiles & 1];
-        {
-          const int c = qt * p.cols + threadIdx.x;
-          float v = INFINITY;
-          if ((int)threadIdx.x < p.cols && c < th) {
-            const float l = __ldg(p.lse + (int64_t)wk.seq * th + c);
-            v = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-          }
-          lse2[threadIdx.x] = v;
+    // ---- epilogue: thread = (query row r, slots 64 * half .. of every chunk)
+    const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemS + 64 * half;
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && wk.next(p)) {
+      for (int qt = 0; ok && qt < n_tiles; ++qt) {
+        const int m = min(kRows, th - qt * kRows);  // rows of this tile
+        const bool dead = (warp & 3) * 32 >= m;     // a warp without rows only keeps step
+        float lse2 = 0.f;
+        bool live = r < m;
+        if (live) {
+          const float l = __ldg(p.lse + (int64_t)wk.seq * th + qt * kRows + r);
+          live = l != -INFINITY;  // a row that saw nothing adds nothing
+          lse2 = l * 1.4426950408889634f;
         }
-        // the tile's lse2 is written; a warp whose wait ran out takes the others along
-        if (named_barrier_or(1, 128, !ok)) {
-          leave = true;
-          break;
-        }
+        // slots that this row's token sees, and the first token
+        const int row_len = wk.len - p.T + 1 + (qt * kRows + r) / p.H, min_len = wk.len - p.T + 1;
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
           const int sb = g & 1;
-          const int64_t s = (int64_t)i * kChunk + threadIdx.x;
-          const bool in = s < wk.len;
-          const bool there = in && pool_row(p.pool, wk.seq, (int32_t)s) >= 0;
-          const int64_t o = (int64_t)wk.seq * p.ld_slots + s;
+          // the first 128 threads finish a slot each
+          const int64_t s = (int64_t)i * kChunk + threadIdx.x, o = (int64_t)wk.seq * p.ld_slots + s;
+          const bool mine = threadIdx.x < kChunk && s < wk.len;
           float old = 0.f;
-          if (in) old = qt > 0 ? p.acc_out[o] : p.acc ? p.decay * p.acc[o] : 0.f;
-          // columns from c_min on see this slot
-          const int64_t beyond = s - ((int64_t)wk.len - p.T);
-          const int c_min = beyond > 0 && in ? (int)min(beyond * p.H, (int64_t)th) - qt * p.cols : 0;
-          const bool masked = __any_sync(0xffffffffu, c_min > 0);
-          if (!(ok = warp_wait(bar(kSFull + sb), (g >> 1) & 1, abort, p.wait_limit_ns))) break;
-          tc_fence_after();
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int c0 = 0; c0 < p.cols; c0 += 32) {
-            uint32_t sv[32];
-            tmem_ld32(lane_addr + kMaxCols * sb + c0, sv);
-            tc_wait_ld();
-            if (c0 + 32 >= p.cols) {
-              tc_fence_before();
-              warp_arrive(bar(kSEmpty + sb));
+          bool there = false;
+          if (mine) {
+            old = qt > 0 ? p.acc_out[o] : p.acc ? p.decay * p.acc[o] : 0.f;
+            there = pool_row(p.pool, wk.seq, (int32_t)s) >= 0;
+          }
+          ok = warp_wait(bar(kSFull + sb), (g >> 1) & 1, abort, p.wait_limit_ns);
+          if (ok) {
+            tc_fence_after();
+            uint32_t sv[64];
+            if (!dead) {
+              tmem_ld64(s_addr + kChunk * sb, sv);
+              tc_wait_ld();
             }
+            tc_fence_before();
+            warp_arrive(bar(kSEmpty + sb));
+            if (!dead) {
+              const int64_t s0 = (int64_t)i * kChunk + 64 * half;
+              const int see = s0 + 64 <= min_len ? 64 : (int)min(max(row_len - s0, (int64_t)0), (int64_t)64);
+              float v[64];
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(lse2 + c0 + c);
-              const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                // columns that hold no query row were loaded as zeros: 0 - inf
-                float x = fmaf(__uint_as_float(sv[c + e]), p.scale_log2, -lv[e]);
-                if (masked && c0 + c + e < c_min) x = -INFINITY;
-                if (lv[e] == INFINITY) x = -INFINITY;
-                sum[e] += ex2_approx(x);
+              for (int c = 0; c < 64; ++c) {
+                const float x = ex2_approx(fmaf(__uint_as_float(sv[c]), p.scale_log2, -lse2));
+                v[c] = live && c < see ? x : 0.f;
               }
+              // sums over the warp's rows: lane l ends with columns l and l + 32
+#pragma unroll
+              for (int grp = 0; grp < 64; grp += 32) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) {
+                  const bool up = (lane & d) != 0;
+#pragma unroll
+                  for (int c = 0; c < d; ++c) {
+                    const float keep = up ? v[grp + c + d] : v[grp + c], give = up ? v[grp + c] : v[grp + c + d];
+                    v[grp + c] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                  }
+                }
+              }
+              misc->part[sb][warp & 3][64 * half + lane] = v[0];
+              misc->part[sb][warp & 3][64 * half + 32 + lane] = v[32];
             }
           }
-          if (in) p.acc_out[o] = there ? old + ((sum[0] + sum[1]) + (sum[2] + sum[3])) : old;
+          // every warp's sums are written; all leave together
+          if (named_barrier_or(1, 32 * kEpiWarps, !ok)) {
+            ok = false;
+            break;
+          }
+          if (mine) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (32 * w < m) sum += misc->part[sb][w][threadIdx.x];
+            p.acc_out[o] = there ? old + sum : old;
+          }
         }
       }
     }
@@ -346,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kMaxCols);
+    tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0 && *abort) report(p.status, DSA_ERR_TIMEOUT);
 }
@@ -373,9 +437,6 @@ extern "C" int dsa_paged_weights(const void* q, const void* kv_pages, const int3
   p.B = B;
   p.T = T;
   p.H = H;
-  const int64_t th = (int64_t)T * H;
-  p.cols = (int)std::min<int64_t>((th + 15) / 16 * 16, kMaxCols);
-  p.places = std::min(kMaxPlaces, (kSmemTotal - kMiscBytes - kKB * p.cols * 128) / kBlockBytes);
   p.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.decay = decay;
@@ -385,19 +446,17 @@ extern "C" int dsa_paged_weights(const void* q, const void* kv_pages, const int3
   p.status = dev_status;
   p.wait_limit_ns = kWaitLimitNs;
   CUtensorMap tq, tk;
-  // rows behind a sequence's own query rows read as zeros
-  const uint64_t dims[3] = {kDQK, (uint64_t)th, (uint64_t)B}, strides[2] = {kDQK * 2, (uint64_t)th * kDQK * 2};
-  const uint32_t box[3] = {64, (uint32_t)p.cols, 1};
-  if (!make_tmap_3d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, kRows,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)n_pages * page_size, kDQK * 2, 64,
                     (uint32_t)p.box, CU_TENSOR_MAP_SWIZZLE_128B))
     return DSA_ERR_CUDA;
   static PerDeviceOnce attr;
   if (attr.run([] {
-        return cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal + 1024);
+        return cudaFuncSetAttribute(paged_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       }) != cudaSuccess)
     return DSA_ERR_CUDA;
   const cudaError_t e = launch_pdl(paged_weights_kernel, dim3((unsigned)device_info().sm_count), dim3(kThreads),
-                                   (size_t)(kSmemTotal + 1024), reinterpret_cast<cudaStream_t>(stream), tq, tk, p);
+                                   (size_t)kSmemBytes, reinterpret_cast<cudaStream_t>(stream), tq, tk, p);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
