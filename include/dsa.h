@@ -237,8 +237,9 @@ int dsa_sparse_mla_noalloc(const void* q, const void* kv, const int32_t* offsets
  * it exists so that a test can make a pipeline wait run out on purpose
  * without faulting or hanging the GPU.
  *
- * The next n_launches attention-stage launches in this process (from
- * dsa_sparse_mla, dsa_decode_step or dsa_sparse_mla_noalloc) initialise their
+ * The next n_launches attention launches in this process (from
+ * dsa_sparse_mla, dsa_decode_step, dsa_sparse_mla_noalloc or dsa_paged_mla)
+ * initialise their
  * query barrier with one expected arrival more than will ever come, and limit
  * every pipeline wait to wait_limit_ns (1 ms to 1 s).  The wait runs out; the
  * kernel stops its pipeline, waits (bounded) for its own copies and tensor
@@ -298,9 +299,13 @@ int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* pag
  *   l_s = scale * q[b,t,h,:576] . kv(b,s)[:576],  s <= lens[b] - T + t;  p = softmax_s(l)
  *   out[b,t,h,:] = sum_s p_s * kv(b,s)[:512];  lse[b,t,h] = log sum_s exp(l_s)
  * Rows that see no slot get out = 0, lse = -inf.
+ * The cache is read once per 128 (token, head) rows of a sequence.  The work
+ * is divided by the lengths found on the device, so ragged batches need no
+ * padding and no plan.  The result does not depend on what else runs; the same
+ * inputs give the same bits.
  * workspace: dsa_paged_mla_workspace_size(B, T, H) bytes, for the current
  * device; its contents need not survive between calls, and calls that may run
- * at the same time need one each.
+ * at the same time (two graphs, two streams) need one each.
  */
 size_t dsa_paged_mla_workspace_size(int B, int T, int H);
 int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,

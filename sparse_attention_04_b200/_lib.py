@@ -335,7 +335,7 @@ def paged_mla(q, kv_pages, page_table, lens, scale, out, lse=None, workspace=Non
     code, o = _out_code(out, (B, T, H, 512), dev)
     ws = None if workspace is None else _arg(workspace, workspace.dtype, workspace.shape, "workspace", dev)
     _run_on(dev, stream, lib.dsa_paged_mla, "dsa_paged_mla", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev), kv, table,
-            ld_table, max_pages, _arg(lens, torch.int32, (B,), "lens", dev), B, T, H, P, n_pages, scale, o, code,
+            ld_table, max_pages, _arg(lens, torch.int32, (B,), "lens", dev), B, T, H, P, n_pages, float(scale), o, code,
             _arg(lse, torch.float32, (B, T, H), "lse", dev), ws, 0 if ws is None else workspace.nbytes,
             _arg(status, torch.int32, (1,), "status", dev))
 
@@ -356,7 +356,7 @@ def paged_weights(q, kv_pages, page_table, lens, lse, scale, acc, acc_out=None, 
     a = o if acc is acc_out else _arg(acc, torch.float32, (B, ld), "acc", dev)
     _run_on(dev, stream, lib.dsa_paged_weights, "dsa_paged_weights", _arg(q, torch.bfloat16, (B, T, H, 576), "q", dev), kv,
             table, ld_table, max_pages, _arg(lens, torch.int32, (B,), "lens", dev),
-            _arg(lse, torch.float32, (B, T, H), "lse", dev), B, T, H, P, n_pages, scale, decay, a, o, ld,
+            _arg(lse, torch.float32, (B, T, H), "lse", dev), B, T, H, P, n_pages, float(scale), float(decay), a, o, ld,
             _arg(status, torch.int32, (1,), "status", dev))
 
 
@@ -372,7 +372,7 @@ def evict_plan(acc, pos, lens, end_pos, budget, recent, new_lens, n_moves, move_
         raise DSAError(1, "evict_plan: move_dst and move_src need a row per sequence")
     a, p, ld = _slots(acc, pos, B, dev)
     _run_on(dev, stream, lib.dsa_evict_plan, "dsa_evict_plan", a, p, _arg(lens, torch.int32, (B,), "lens", dev),
-            _arg(end_pos, torch.int32, (B,), "end_pos", dev), B, ld, budget, recent,
+            _arg(end_pos, torch.int32, (B,), "end_pos", dev), B, ld, int(budget), int(recent),
             _arg(new_lens, torch.int32, (B,), "new_lens", dev), _arg(n_moves, torch.int32, (B,), "n_moves", dev),
             _arg(move_dst, torch.int32, moves, "move_dst", dev), _arg(move_src, torch.int32, moves, "move_src", dev),
             moves[1], _arg(status, torch.int32, (1,), "status", dev))

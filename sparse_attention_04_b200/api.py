@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .inputs import D_V, Inputs
+from .inputs import D_QK, D_V, Inputs
 
 
 @dataclasses.dataclass
@@ -170,6 +170,76 @@ class HostDecodeStep:
                             lse=st.lse, workspace=self._ws_mla, status=st.status)
         _lib.copy_device_to_host(self.host_out, st.out)
         return self.host_out
+
+
+class PagedLatentCache:
+    """A paged latent cache of B sequences and what a decode step does with it:
+
+        out = cache.append(kv_new).attend(q, scale)    # attention over all of it
+        cache.collect(q, scale, decay)                 # attention weight per slot
+        cache.evict(budget, recent)                    # keep the heaviest and newest
+
+    Lengths, positions and the eviction plan stay on the device, so that the
+    whole step can be captured in one CUDA graph.  Every sequence has page
+    lists for `slots` slots; a scheduler that hands pages out writes its own
+    numbers into page_table.  Set lens (and end_pos, the tokens seen so far)
+    after filling the first rows, or append the prompt in calls of T tokens.
+    An append beyond `slots` is left out and reported in status.
+
+    kv_pages [pages, page_size, 576] bf16, page_table [B, pages per sequence],
+    lens and end_pos [B], acc and pos [B, slots] (see include/dsa.h)."""
+
+    def __init__(self, B: int, slots: int, T: int = 1, H: int = 128, page_size: int = 64, max_moves: Optional[int] = None,
+                 out_dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        pages = -(-slots // page_size)
+        ld = -(-slots // 4) * 4
+        self.B, self.T, self.H, self.slots = B, T, H, slots
+        self.kv_pages = torch.empty((B * pages, page_size, D_QK), dtype=torch.bfloat16, device=dev)
+        self.page_table = torch.arange(B * pages, dtype=torch.int32, device=dev).view(B, pages)
+        self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.end_pos = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.acc = torch.zeros((B, ld), dtype=torch.float32, device=dev)
+        self.pos = torch.zeros((B, ld), dtype=torch.int32, device=dev)
+        self.out = torch.empty((B, T, H, D_V), dtype=out_dtype, device=dev)
+        self.lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        with torch.cuda.device(self.lens.device):
+            nbytes = _lib.paged_mla_workspace_size(B, T, H)
+        self.workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        moves = max(1, max_moves if max_moves is not None else slots // 2)
+        self.new_lens, self.n_moves = torch.zeros_like(self.lens), torch.zeros_like(self.lens)
+        self.move_dst = torch.empty((B, moves), dtype=torch.int32, device=dev)
+        self.move_src = torch.empty((B, moves), dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def append(self, kv_new):
+        """The T newest tokens' rows [B,T,576] of every sequence."""
+        self.lens.add_(kv_new.shape[1])
+        self.end_pos.add_(kv_new.shape[1])
+        _lib.paged_append(kv_new, self.kv_pages, self.page_table, self.lens, acc=self.acc, pos=self.pos,
+                          end_pos=self.end_pos, status=self.status)
+        return self
+
+    def attend(self, q, scale):
+        """Attention of q [B,T,H,576] over each whole cache: out [B,T,H,512]; lse beside it."""
+        _lib.paged_mla(q, self.kv_pages, self.page_table, self.lens, scale, self.out, lse=self.lse,
+                       workspace=self.workspace, status=self.status)
+        return self.out
+
+    def collect(self, q, scale, decay=1.0):
+        """Adds the weight that the slots got from the last attend's q to acc."""
+        _lib.paged_weights(q, self.kv_pages, self.page_table, self.lens, self.lse, scale, self.acc, decay=decay,
+                           status=self.status)
+        return self.acc
+
+    def evict(self, budget, recent=0):
+        """Cuts every sequence to `budget` slots; the `recent` newest tokens stay."""
+        _lib.evict_plan(self.acc, self.pos, self.lens, self.end_pos, budget, recent, self.new_lens, self.n_moves,
+                        self.move_dst, self.move_src, status=self.status)
+        _lib.paged_move(self.kv_pages, self.page_table, self.n_moves, self.move_dst, self.move_src, acc=self.acc,
+                        pos=self.pos, status=self.status)
+        self.lens.copy_(self.new_lens)
+        return self.lens
 
 
 def decode_step(inp: Inputs, step: Optional[DecodeStep] = None) -> StepResult:

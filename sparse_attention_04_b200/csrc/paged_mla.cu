@@ -529,7 +529,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // CTA 1's last arrivals here must land before this CTA exits
       for (uint32_t k = j > kPBufs ? j - kPBufs : 0; ok && k < j; ++k)
         ok = warp_wait<true>(bar(kPvDone + k % kPBufs), (k / kPBufs) & 1, abort, p.wait_limit_ns);
-      if (*abort) give_up();
+      if (*abort) {
+        give_up();
+        // nobody here can see the last stores land in the partner: 50 us are
+        // ample, and the partner does not leave before this CTA
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 50000ull) {
+        }
+      }
     } else if (warp < 8) {
       // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
       const int h = (warp & 3) * 32 + lane, half = warp >> 2;

@@ -633,3 +633,118 @@ def test_decode_with_eviction_step_by_step(cuda_device, graph):
             c.lens_py[b] = m
             assert torch.equal(c.of(b), caches[b]), (i, b)
             assert pos[b, :m].tolist() == places[b], (i, b)
+
+
+def test_cache_object_runs_the_same_calls(cuda_device):
+    """api.PagedLatentCache against the calls it is made of, over a prompt and
+    steps with eviction; the padded (empty) case is a cache that was never filled."""
+    from sparse_attention_04_b200 import api
+    L, dev, B, H = _lib(), cuda_device, 2, 16
+    g = torch.Generator(device=dev).manual_seed(5)
+    one = api.PagedLatentCache(B, 40, T=2, H=H, page_size=16, out_dtype=torch.float32)
+    assert torch.all(one.attend(torch.ones(B, 2, H, D, dtype=torch.bfloat16, device=dev), SCALE) == 0)
+    kv, lens, end = one.kv_pages.clone().zero_(), torch.zeros_like(one.lens), torch.zeros_like(one.lens)
+    one.kv_pages.zero_()
+    acc, pos = torch.zeros_like(one.acc), torch.zeros_like(one.pos)
+    ws = torch.empty(L.paged_mla_workspace_size(B, 2, H), dtype=torch.uint8, device=dev)
+    out, lse = torch.empty(B, 2, H, DV, device=dev), torch.empty(B, 2, H, device=dev)
+    t = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+    new, n, dst, src = t(B), t(B), t(B, 20), t(B, 20)
+    for step in range(25):
+        x = torch.randn(B, 2, D, generator=g, device=dev).to(torch.bfloat16)
+        q = torch.randn(B, 2, H, D, generator=g, device=dev).to(torch.bfloat16)
+        got = one.append(x).attend(q, SCALE).clone()
+        one.collect(q, SCALE, 0.9)
+        one.evict(36, 4)
+        lens += 2
+        end += 2
+        L.paged_append(x, kv, one.page_table, lens, acc=acc, pos=pos, end_pos=end)
+        L.paged_mla(q, kv, one.page_table, lens, SCALE, out, lse=lse, workspace=ws)
+        L.paged_weights(q, kv, one.page_table, lens, lse, SCALE, acc, decay=0.9)
+        L.evict_plan(acc, pos, lens, end, 36, 4, new, n, dst, src)
+        L.paged_move(kv, one.page_table, n, dst, src, acc=acc, pos=pos)
+        lens.copy_(new)
+        assert torch.equal(got, out) and torch.equal(one.acc, acc) and torch.equal(one.pos, pos), step
+        assert torch.equal(one.lens, lens) and torch.equal(one.kv_pages, kv), step
+    assert lens.tolist() == [36, 36] and int(one.status.item()) == 0
+
+
+def test_attention_wait_runs_out_then_next_call_is_correct(cuda_device):
+    """The timeout path (test hook): a bounded wait that never comes true ends the
+    launch with DSA_ERR_TIMEOUT, and the launch after it is right."""
+    L = _lib()
+    c = Cache(cuda_device, [3000, 40, 0, 700], 64, seed=40)
+    q = _q(c, 4, 1, 128)
+    L.debug_stall_attention(1, 5_000_000)
+    try:
+        _, _, st = _attend(c, q)
+    finally:
+        L.debug_stall_attention(0, 0)
+    assert st == 5
+    out, lse, st = _attend(c, q)
+    assert st == 0
+    _check_attention(c, q, out, lse)
+
+
+def test_two_streams_and_two_graphs_with_a_workspace_each(cuda_device):
+    """Calls that overlap: the results are those of the calls alone."""
+    L = _lib()
+    cs = [Cache(cuda_device, lens, 32, seed=50 + i) for i, lens in enumerate(([5000, 300], [77, 9000]))]
+    qs = [_q(c, 2, 1, 64) for c in cs]
+    want = [_attend(c, q)[:2] for c, q in zip(cs, qs)]
+    n = L.paged_mla_workspace_size(2, 1, 64)
+    got, graphs, streams = [], [], [torch.cuda.Stream() for _ in cs]
+    for c, q, s in zip(cs, qs, streams):
+        out, lse, ws = torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), torch.empty(n, dtype=torch.uint8, device=c.dev)
+        acc = torch.zeros(2, 9000, device=c.dev)
+        got.append((out, lse, acc, ws))
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                L.paged_mla(q, c.kv, c.table, c.lens, SCALE, out, lse=lse, workspace=ws)
+                L.paged_weights(q, c.kv, c.table, c.lens, lse, SCALE, None, acc_out=acc)
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (out, lse, acc, _), w in zip(cs, got, want):
+        assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+        alone = torch.zeros_like(acc)
+        L.paged_weights(qs[cs.index(c)], c.kv, c.table, c.lens, lse, SCALE, None, acc_out=alone)
+        assert torch.equal(acc, alone)
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """Kernel attributes are set on the first call; that call may be inside a capture."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from sparse_attention_04_b200 import _lib as L
+dev = torch.device("cuda:0")
+kv = torch.randn(4, 64, 576, device=dev).to(torch.bfloat16)
+table = torch.arange(4, dtype=torch.int32, device=dev).view(1, 4)
+lens = torch.tensor([200], dtype=torch.int32, device=dev)
+q = torch.randn(1, 1, 128, 576, device=dev).to(torch.bfloat16)
+out, lse = torch.zeros(1, 1, 128, 512, device=dev), torch.zeros(1, 1, 128, device=dev)
+acc = torch.zeros(1, 256, device=dev)
+i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+new, n, dst, src = i(1), i(1), i(1, 128), i(1, 128)
+ws = torch.empty(L.paged_mla_workspace_size(1, 1, 128), dtype=torch.uint8, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    L.paged_mla(q, kv, table, lens, 0.07, out, lse=lse, workspace=ws)
+    L.paged_weights(q, kv, table, lens, lse, 0.07, acc)
+    L.evict_plan(acc, None, lens, None, 100, 0, new, n, dst, src)
+    L.paged_move(kv, table, n, dst, src, acc=acc)
+g.replay()
+torch.cuda.synchronize()
+assert int(new) == 100 and abs(float(acc[0, :200].sum())) > 100 and float(out.abs().sum()) > 0
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
