@@ -287,6 +287,59 @@ def test_attention_of_a_wider_page_table(cuda_device):
     assert st == 0 and torch.equal(out, ref) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("T,H,lens", [(300, 128, [300, 900]), (1000, 2, [1000, 1010, 3]), (129, 1, [400, 129]),
+                                      (10, 13, [2000, 9, 64]), (65, 64, [65, 500])])
+def test_attention_of_many_new_tokens(cuda_device, T, H, lens):
+    """Prompts: several tiles of tokens per sequence, the last one partly filled,
+    tokens before the sequence's first slot."""
+    c = Cache(cuda_device, lens, 16, seed=T)
+    q = _q(c, len(lens), T, H)
+    out, lse, st = _attend(c, q)
+    assert st == 0
+    _check_attention(c, q, out, lse)
+    _, st = _check_weights(c, q, lse, torch.rand(len(lens), 2000, generator=c.g, device=c.dev), 0.5)
+    assert st == 0
+
+
+def test_attention_with_nothing_but_padding_and_with_more_sequences_than_clusters(cuda_device):
+    c = Cache(cuda_device, [0] * 5, 16, seed=60)
+    q = _q(c, 5, 1, 128)
+    out, lse, st = _attend(c, q)
+    assert st == 0 and torch.all(out == 0) and torch.all(lse == float("-inf"))
+    lens = [0, 1] * 1000 + [4000]
+    c = Cache(cuda_device, lens, 16, seed=61)
+    q = _q(c, len(lens), 1, 16)
+    out, lse, st = _attend(c, q)
+    assert st == 0
+    some = [0, 1, 2, 999, 1000, 1999, 2000]
+    one = Cache.__new__(Cache)
+    for b in some:
+        one.__dict__.update(c.__dict__)
+        one.lens_py, one.table = [lens[b]], c.table[b:b + 1]
+        _check_attention(one, q[b:b + 1], out[b:b + 1], lse[b:b + 1])
+    # every sequence of one slot returns that slot's row, rounded
+    ones = torch.arange(1, 2000, 2, device=c.dev)
+    rows = c.flat[c.table[ones, 0].long() * 16][:, None, None, :DV]
+    assert torch.equal(out[ones], rows.expand(-1, 1, 16, -1))
+
+
+@pytest.mark.parametrize("H,T", [(128, 1), (16, 4)])
+def test_attention_over_infinities_and_huge_values(cuda_device, H, T):
+    """Values near the type's largest in the cache, infinities in slots behind the
+    end; nothing overflows on the way (partials are scaled)."""
+    c = Cache(cuda_device, [9000, 100], 64, seed=62)
+    c.kv.copy_(torch.where(c.kv.isnan(), torch.full_like(c.kv, float("inf")), c.kv))
+    for b, n in enumerate(c.lens_py):
+        rows = c.rows(b, torch.arange(n, device=c.dev))
+        c.flat[rows, :256] *= 2.0 ** 100
+        c.flat[rows, 256:512] *= 2.0 ** -100
+    q = _q(c, 2, T, H)
+    q[..., :512] = 0  # the logits come from the last 64 columns
+    out, lse, st = _attend(c, q, torch.float32)
+    assert st == 0
+    _check_attention(c, q, out, lse)
+
+
 # ---------------------------------------------------------------- weights
 
 def _check_weights(c, q, lse, acc, decay, skip=None, in_place=False):
