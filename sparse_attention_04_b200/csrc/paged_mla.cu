@@ -20,7 +20,8 @@
 // 512 fp32 columns), so the pair divides the work by role:
 //   CTA 0 (QK side): query blocks 0-7 (64 columns each) in TMEM, block 8 in
 //     shared memory; a chunk's rows arrive by TMA as nine 128 x 64 blocks in a
-//     ring of eight; S = Q.K^T (N = 128) goes to one of two TMEM buffers.
+//     ring of three places of three; S = Q.K^T (N = 128) goes to one of two
+//     TMEM buffers.
 //     Eight softmax warps, thread = (head, half of the chunk's slots); the
 //     halves' maxima meet in shared memory, P is rounded to bf16 (the tensor
 //     core's operand; its sum l is kept unrounded in fp32) and two warps store
@@ -35,6 +36,21 @@
 // are asked for outside the tensor and arrive as zeros; slots behind the end
 // inside the last box are zeroed in CTA 1 before the product (their P is 0,
 // but they may hold NaN) and masked in CTA 0.
+//
+// What bounds it (B200).  32 sequences of 8K to 128K slots, 128 heads: 0.54 ms
+// in a short run (4.3 TB/s, 1.03 PFLOP/s) and 0.64 ms in a long one, where the
+// 1000 W cap holds the SM clock near 1.2 GHz; a chunk takes about 3400 cycles,
+// 2304 of them QK products.  Without the loads the same kernel takes 0.37 ms,
+// with all of them answered by L2 0.42 ms.  What the steps to it were worth:
+// MMAs issued under an elected-lane predicate, waits that suspend, and small
+// code in the two issuing loops (instruction fetch: unrolled nine times they
+// took twice as long) 0.83 -> 0.56 ms; no arrival on the partner's barriers on
+// the way of a message (it flushes the thread's earlier stores first, 2000
+// cycles) 0.70 -> 0.61.  Measured slower: requesting later chunks into L2 ahead
+// (0.55 -> 0.63 ms and more), P through the copy engine (behind the block loads
+// in its queue).  One 2K row takes 23 us and one 32K row 31 us, most of it
+// latency: query into TMEM, one chunk through both CTAs, the partial's 262 KB
+// at about 37 bytes a cycle, the joining kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -51,7 +67,7 @@ constexpr int kSub = 64;                 // slots per message to CTA 1
 constexpr int kKB = kDQK / 64;           // 64-column blocks of a row: 9
 constexpr int kQBlockBytes = 128 * 128;             // a 64-column block of the query, 128 heads
 constexpr int kVBlockBytes = kSub * 128;            // a 64-column block of 64 rows
-constexpr int kRowUnits = 2;             // what a row costs besides its chunks, in chunks
+constexpr int kRowUnits = 2;             // what a tile costs besides its chunks, in chunks (64 rows of 2K slots: 76.2 us; 1: 79.2, 4: 78.2)
 
 constexpr int kThreads = 384;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kSendWarp = 10;
@@ -1161,11 +1177,16 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   if (n > 1) {
-    // eight partials and more per row on average: eight warps share them
-    const bool few = p.n_rows <= n / 8;
-    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8) * (few ? 8 : 1) / kCombineWarps;
+    // Warps that share a row's partials, by how many a row has at most (one
+    // row of 32K: 30.9 us with eight, 33.0 with four, 37.0 with two; two rows
+    // 30.9, 28.9, 30.8; eight rows 51.5, 47.5, 43.5 and 42.8 with one, because
+    // the tasks then fill the card several times over).
+    const int per_row = n / p.n_rows, split = per_row >= 64 ? 8 : per_row >= 16 ? 4 : 1;
+    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8) * split / kCombineWarps;
     const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * kCombineWarps);
-    const auto kernel = few ? paged_mla_combine_kernel<8> : paged_mla_combine_kernel<1>;
+    const auto kernel = split == 8   ? paged_mla_combine_kernel<8>
+                        : split == 4 ? paged_mla_combine_kernel<4>
+                                     : paged_mla_combine_kernel<1>;
     if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float4*)p.part_o,
                    n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;
