@@ -49,10 +49,11 @@
 // cycles) 0.70 -> 0.61.  Measured slower: requesting later chunks into L2 ahead
 // (0.55 -> 0.63 ms and more), P through the copy engine (behind the block loads
 // in its queue).  One 2K row takes 23 us and one 32K row 31 us, most of it
-// latency: query into TMEM, one chunk through both CTAs, the partial's 262 KB
-// at about 37 bytes a cycle, the joining kernel.
+// latency: query into TMEM, one chunk through both CTAs, the partial's stores,
+// the joining kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -153,7 +154,8 @@ struct PagedMlaParams {
   float* lse;
   CutRow* cut;       // [n_clusters]
   float* part_ml;    // [2 * n_clusters][2][tp * H]: maximum, sum
-  float4* part_o;    // [2 * n_clusters][128][tp * H][4], unnormalised
+  float* part_sc;    // [2 * n_clusters][16][tp * H]: what 32 columns are to be multiplied by
+  uint4* part_o;     // [2 * n_clusters][64][tp * H][8] fp16, unnormalised
   int32_t* status;
   int debug_stall;
   uint64_t wait_limit_ns;
@@ -222,6 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     if (lane == 0) {
       tma_prefetch_desc(rank == 0 ? &tm_k : &tm_v);
+      if (rank == 0) tma_prefetch_desc(&tm_q);
       mbar_init(bar(kQFull), 1 + p.debug_stall);
       mbar_init(bar(kQFree), 1);
       for (int i = 0; i < kKSlots; ++i) {
@@ -278,12 +281,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) misc->warp_sum[warp] = inc;
     __syncthreads();
-    int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int64_t v = misc->warp_sum[w];
-      if (w < warp) before += v;
-      total += v;
+    // every warp adds the warps' sums up for itself
+    int64_t total = lane < kThreads / 32 ? misc->warp_sum[lane] : 0, before = lane < warp ? total : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
     }
+    before += inc - mine;
     const int64_t share = ceil_div(total, p.n_clusters), w0 = share * cl;
     if (threadIdx.x == 0) {
       misc->total_units = total;
@@ -847,12 +852,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool whole = wk.hi - wk.lo == wk.chunks;
         const float mul = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
         const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
-        // Partials: fp32, [column / 4][row][4], so that a warp's stores are whole
-        // lines.
+        // Partials: fp16, each row's 32 columns scaled by the power of two that
+        // brings the largest of them to [1, 2): 11 bits, against the 8 that P
+        // has and a bf16 output keeps, and half the bytes of fp32.  (An SM
+        // writes 28 bytes a cycle, however it writes: a 128-row fp32 partial
+        // takes 9000 cycles.)  [column / 8][row][8], so that a warp's stores
+        // are whole lines.
         // Finished rows: 32 bytes of 32 rows at a time through shared memory,
         // so that two lanes write a row's piece.
         const int pm = p.tp * p.H;  // rows a partial has room for
-        float4* const pout = p.part_o + part * pm * (kDV / 4) + h;
+        uint4* const pout = p.part_o + part * pm * (kDV / 8) + h;
         uint8_t* const rowp = ostage + lane * 32;
         const int sw = (lane >> 2) & 1;
         const int elt = p.out_bf16 ? 2 : 4;
@@ -883,11 +892,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (!whole) {
             if (h < wk.m) {
+              float big = 0.f;
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
-                pout[(int64_t)(c0 / 4 + c) * pm] =
-                    make_float4(__uint_as_float(ov[4 * c]), __uint_as_float(ov[4 * c + 1]), __uint_as_float(ov[4 * c + 2]),
-                                __uint_as_float(ov[4 * c + 3]));
+              for (int c = 0; c < 32; ++c) big = fmaxf(big, fabsf(__uint_as_float(ov[c])));
+              if (big == INFINITY) {  // the largest finite one decides; infinities stay what they are
+                big = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  const float v = fabsf(__uint_as_float(ov[c]));
+                  if (v < INFINITY) big = fmaxf(big, v);
+                }
+              }
+              const int e = min(max((int)(__float_as_uint(big) >> 23), 1), 253);  // biased exponent
+              const float scale = __uint_as_float((uint32_t)(254 - e) << 23);
+              p.part_sc[(part * (kDV / 32) + c0 / 32) * pm + h] = __uint_as_float((uint32_t)e << 23);  // 1 / scale
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 t2 = __floats2half2_rn(__uint_as_float(ov[8 * c + 2 * e]) * scale,
+                                                       __uint_as_float(ov[8 * c + 2 * e + 1]) * scale);
+                  w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
+                }
+                pout[(int64_t)(c0 / 8 + c) * pm] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
             }
           } else if (p.out_bf16) {
 #pragma unroll 1
@@ -956,8 +985,8 @@ constexpr int kMaxClusters = 128;
 template <int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
-                             const float4* __restrict__ part_o, int n_clusters, int pm, void* out, int out_bf16,
-                             float* lse) {
+                             const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_clusters, int pm,
+                             void* out, int out_bf16, float* lse) {
   constexpr int kGroups = kCombineWarps / SPLIT;  // column groups per task
   constexpr int kFlight = 8;                       // partials a thread has in flight
   __shared__ CutRow s_cut[kMaxClusters];
@@ -988,21 +1017,21 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     float M = -INFINITY, l = 0.f;
     if (h < c.m) {
       for (int i0 = sub; i0 < c.count; i0 += SPLIT * kFlight) {
-        float4 o[kFlight][2];
-        float m[kFlight], li[kFlight], top = M;
+        uint4 o[kFlight];
+        float m[kFlight], li[kFlight], sc[kFlight], top = M;
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int i = i0 + SPLIT * k;
           m[k] = -INFINITY;
-          li[k] = 0.f;
-          o[k][0] = o[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          li[k] = sc[k] = 0.f;
+          o[k] = make_uint4(0u, 0u, 0u, 0u);
           if (i < c.count) {
             // the first partial is its cluster's second, the others are their clusters' first
             const int64_t part = 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0);
             m[k] = __ldg(part_ml + 2 * part * pm + h);
             li[k] = __ldg(part_ml + (2 * part + 1) * pm + h);
-            o[k][0] = __ldg(part_o + (part * (kDV / 4) + 2 * grp) * pm + h);
-            o[k][1] = __ldg(part_o + (part * (kDV / 4) + 2 * grp + 1) * pm + h);
+            sc[k] = __ldg(part_sc + (part * (kDV / 32) + grp / 4) * pm + h);
+            o[k] = __ldg(part_o + (part * (kDV / 8) + grp) * pm + h);
           }
         }
 #pragma unroll
@@ -1015,16 +1044,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
         for (int e = 0; e < 8; ++e) acc[e] *= a;
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
-          const float w = exp2f(m[k] - off);
+          const float w = exp2f(m[k] - off), ws = w * sc[k];
           l = fmaf(w, li[k], l);
-          acc[0] = fmaf(w, o[k][0].x, acc[0]);
-          acc[1] = fmaf(w, o[k][0].y, acc[1]);
-          acc[2] = fmaf(w, o[k][0].z, acc[2]);
-          acc[3] = fmaf(w, o[k][0].w, acc[3]);
-          acc[4] = fmaf(w, o[k][1].x, acc[4]);
-          acc[5] = fmaf(w, o[k][1].y, acc[5]);
-          acc[6] = fmaf(w, o[k][1].z, acc[6]);
-          acc[7] = fmaf(w, o[k][1].w, acc[7]);
+          const uint32_t w4[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+            acc[2 * e] = fmaf(ws, f.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(ws, f.y, acc[2 * e + 1]);
+          }
         }
       }
     }
@@ -1110,7 +1138,7 @@ int tokens_per_tile(int T, int H) { return std::max(1, std::min(T, 128 / H)); }
 
 size_t paged_workspace(int T, int H) {
   const size_t n = (size_t)paged_clusters(), m = (size_t)tokens_per_tile(T, H) * H;
-  return n * sizeof(CutRow) + 2 * n * m * kDV * sizeof(float) + 2 * n * m * 2 * sizeof(float);
+  return n * sizeof(CutRow) + 2 * n * m * kDV * sizeof(__half) + 2 * n * m * (2 + kDV / 32) * sizeof(float);
 }
 
 }  // namespace
@@ -1154,8 +1182,9 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.lse = lse;
   p.cut = reinterpret_cast<CutRow*>(workspace);
   const size_t pm = (size_t)p.tp * H;
-  p.part_o = reinterpret_cast<float4*>(p.cut + n);
-  p.part_ml = reinterpret_cast<float*>(p.part_o + 2 * n * pm * (kDV / 4));
+  p.part_o = reinterpret_cast<uint4*>(p.cut + n);
+  p.part_ml = reinterpret_cast<float*>(p.part_o + 2 * n * pm * (kDV / 8));
+  p.part_sc = p.part_ml + 2 * n * pm * 2;
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
   p.wait_limit_ns = debug.wait_limit_ns;
@@ -1187,7 +1216,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
     const auto kernel = split == 8   ? paged_mla_combine_kernel<8>
                         : split == 4 ? paged_mla_combine_kernel<4>
                                      : paged_mla_combine_kernel<1>;
-    if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float4*)p.part_o,
+    if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float*)p.part_sc, (const uint4*)p.part_o,
                    n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;
   }

@@ -145,12 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) misc->warp_sum[warp] = inc;
     __syncthreads();
-    int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int64_t v = misc->warp_sum[w];
-      if (w < warp) before += v;
-      total += v;
+    // every warp adds the warps' sums up for itself
+    int64_t total = lane < kThreads / 32 ? misc->warp_sum[lane] : 0, before = lane < warp ? total : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
     }
+    before += inc - mine;
     const int64_t share = ceil_div(total, (int)gridDim.x), w0 = share * blockIdx.x;
     if (threadIdx.x == 0) {
       misc->total_units = total;

@@ -8,8 +8,10 @@ A logit is a sum of 576 exact products: its fp32 error is at most
 (2u: the tensor core may truncate), and the exponent adds 4u * |x| + 2^-22 for
 scaling, subtraction and ex2.  A weight p is then off by the factor
 exp(2 (d + 4u|x| + 2^-22)) - 1 against another row's sum.  In the output every p
-is rounded once to bf16 (e), sums in fp32 add n * 2u at most, and a bf16 output
-is rounded once more (e)."""
+is rounded once to bf16 (e), sums in fp32 add n * 2u at most, a row that several
+clusters share has its partials in fp16 (half a step 2^-11 of the value, or of
+2^-14 times the largest of 32 columns where that is more), and a bf16 output is
+rounded once more (e)."""
 import pytest
 import torch
 
@@ -108,11 +110,12 @@ def _check_attention(c, q, out, lse, scale=SCALE, skip=None):
             p = x.softmax(1)
             ref, spread = p @ k[:, :DV], p @ k[:, :DV].abs()
             f = _factor(scale, k, qq, x)
-            tol = (f + E + n * 2 * U) * spread * 1.01
+            top = spread.view(H, -1, 32).amax(2, keepdim=True).expand(-1, -1, 32).reshape(H, -1)
+            tol = ((f + E + n * 2 * U) * spread + 2.0 ** -11 * torch.maximum(spread, 2.0 ** -14 * top)) * 1.01
             if out.dtype == torch.bfloat16:
                 tol = tol + E * (ref.abs() + tol)
             err = (out[b, t].double() - ref).abs()
-            assert torch.all(err <= tol + 1e-30), (b, t, n, float((err / (tol + 1e-30)).max()))
+            assert torch.all(err <= tol), (b, t, n, float((err / (tol + 1e-300)).max()))
             ref_lse = x.logsumexp(1)
             tol_lse = (f[:, 0] + n * 2 * U) * 1.01 + 4 * U * (ref_lse.abs() + 30)
             err = (lse[b, t].double() - ref_lse).abs()
@@ -333,6 +336,7 @@ def test_attention_over_infinities_and_huge_values(cuda_device, H, T):
         rows = c.rows(b, torch.arange(n, device=c.dev))
         c.flat[rows, :256] *= 2.0 ** 100
         c.flat[rows, 256:512] *= 2.0 ** -100
+        c.flat[rows, 300:304] *= 2.0 ** 12  # beside much smaller columns
     q = _q(c, 2, T, H)
     q[..., :512] = 0  # the logits come from the last 64 columns
     out, lse, st = _attend(c, q, torch.float32)
