@@ -858,25 +858,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // writes 28 bytes a cycle, however it writes: a 128-row fp32 partial
         // takes 9000 cycles.)  [column / 8][row][8], so that a warp's stores
         // are whole lines.
-        // Finished rows: 32 bytes of 32 rows at a time through shared memory,
-        // so that two lanes write a row's piece.
+        // Finished rows: 64 bytes of 16 rows at a time through shared memory,
+        // so that four lanes write a row's piece.
         const int pm = p.tp * p.H;  // rows a partial has room for
         uint4* const pout = p.part_o + part * pm * (kDV / 8) + h;
-        uint8_t* const rowp = ostage + lane * 32;
-        const int sw = (lane >> 2) & 1;
         const int elt = p.out_bf16 ? 2 : 4;
         uint8_t* const gout =
             reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.q0 + (warp & 3) * 32) * (int64_t)(kDV * elt);
-        auto flush = [&](int col_byte) {
-          __syncwarp();
+        // 64 bytes of every row (four pieces per lane), 16 rows at a time
+        auto put = [&](const uint4 (&piece)[4], int col_byte) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int rr = 16 * u + (lane >> 1), c = lane & 1;
-            const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 32 + ((c ^ ((rr >> 2) & 1)) << 4));
-            if ((warp & 3) * 32 + rr < wk.m)
-              *reinterpret_cast<uint4*>(gout + rr * (kDV * elt) + col_byte + 16 * c) = v;
+          for (int hf = 0; hf < 2; ++hf) {
+            if ((lane >> 4) == hf) {
+              const int rr = lane & 15;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(ostage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)) = piece[c];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int rr = 8 * u + (lane >> 2), c = lane & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(ostage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+              if ((warp & 3) * 32 + 16 * hf + rr < wk.m)
+                *reinterpret_cast<uint4*>(gout + (16 * hf + rr) * (kDV * elt) + col_byte + 16 * c) = v;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         };
 #pragma unroll 1
         for (int c0 = col0; c0 < col0 + 256; c0 += 32) {
@@ -919,31 +927,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             }
           } else if (p.out_bf16) {
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-              // (constant register indexes: both halves are spelled out by the select)
+            uint4 piece[4];
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t w4[4];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w4[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t lo = hf ? ov[16 + 8 * c + 2 * e] : ov[8 * c + 2 * e];
-                  const uint32_t hi = hf ? ov[16 + 8 * c + 2 * e + 1] : ov[8 * c + 2 * e + 1];
-                  const __nv_bfloat162 t2 = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
-                  w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
-                }
-                *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 t2 =
+                    __floats2bfloat162_rn(__uint_as_float(ov[8 * c + 2 * e]), __uint_as_float(ov[8 * c + 2 * e + 1]));
+                w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
               }
-              flush(c0 * 2 + hf * 32);
+              piece[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
+            put(piece, c0 * 2);
           } else {
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
+            for (int hf = 0; hf < 2; ++hf) {
+              uint4 piece[4];
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint4*>(rowp + ((c ^ sw) << 4)) =
-                    make_uint4(ov[8 * q4 + 4 * c], ov[8 * q4 + 4 * c + 1], ov[8 * q4 + 4 * c + 2], ov[8 * q4 + 4 * c + 3]);
-              flush(c0 * 4 + q4 * 32);
+              for (int c = 0; c < 4; ++c)
+                piece[c] = make_uint4(ov[16 * hf + 4 * c], ov[16 * hf + 4 * c + 1], ov[16 * hf + 4 * c + 2], ov[16 * hf + 4 * c + 3]);
+              put(piece, c0 * 4 + hf * 64);
             }
           }
         }
