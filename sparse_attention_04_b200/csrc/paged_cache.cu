@@ -3,7 +3,9 @@
 //
 // Both only move bytes: a token is one 1152-byte row (576 bf16) read and
 // written, plus its acc and pos entries.  HBM bounds them for prompts and
-// large evictions, launch latency for single steps.
+// large evictions, launch latency for single steps.  B200: 8 prompts of 4096
+// tokens (75.8 MB) in 14.5 us, 98 K moves of random rows (461 MB) in 94 us, 4.9
+// TB/s; four rows in flight per warp instead of one measured the same.
 #include <algorithm>
 
 #include "paged.cuh"

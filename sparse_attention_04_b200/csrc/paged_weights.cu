@@ -18,6 +18,9 @@
 // fp32 and in a fixed order.  Every CTA takes an equal, contiguous part of the
 // list of all sequences' 128-slot chunks.
 //
+// B200: 16 sequences of 1K to 65K slots, 128 heads (560 K slots, 644 MB): 106 us
+// in a row, 119 with changing inputs, 6.1 and 5.4 TB/s; one 32K sequence 12 us.
+//
 // Roles: warps 0-7 epilogue, warp 8 loader, warp 9 TMEM allocator and MMA
 // issuer.  S has two TMEM buffers, so that the exponentials of a chunk run
 // beside the products of the next.
