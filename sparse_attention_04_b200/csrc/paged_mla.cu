@@ -850,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float l = l_half[0] + l_half[1];
         const bool whole = wk.hi - wk.lo == wk.chunks;
-        const float mul = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
+        const float mul = l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
         const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
         // Partials: fp16, each row's 32 columns scaled by the power of two that
         // brings the largest of them to [1, 2): 11 bits, against the 8 that P
@@ -893,7 +893,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld32(lane_addr + c0, ov);
             tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = l == 0.f && whole ? 0u : __float_as_uint(__uint_as_float(ov[c]) * mul);
+            for (int c = 0; c < 32; c += 2) {
+              if (!whole) break;
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])), make_float2(mul, mul));
+              ov[c] = __float_as_uint(v.x);
+              ov[c + 1] = __float_as_uint(v.y);
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
@@ -919,8 +924,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t w4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const __half2 t2 = __floats2half2_rn(__uint_as_float(ov[8 * c + 2 * e]) * scale,
-                                                       __uint_as_float(ov[8 * c + 2 * e + 1]) * scale);
+                  const float2 v = __fmul2_rn(make_float2(__uint_as_float(ov[8 * c + 2 * e]), __uint_as_float(ov[8 * c + 2 * e + 1])),
+                                              make_float2(scale, scale));
+                  const __half2 t2 = __floats2half2_rn(v.x, v.y);
                   w4[e] = *reinterpret_cast<const uint32_t*>(&t2);
                 }
                 pout[(int64_t)(c0 / 8 + c) * pm] = make_uint4(w4[0], w4[1], w4[2], w4[3]);

@@ -11,7 +11,7 @@
 // through, four places of three 128-row x 64-column blocks (192 KB: HBM answers
 // in about 2 us under load, so an SM has to keep 90 KB and more in flight.
 // With the query in shared memory as the B operand, 80 KB of ring were left:
-// 140 us against 112 for 16 ragged sequences of 560 K slots in all).
+// 140 us against 106 for 16 ragged sequences of 560 K slots in all).
 // A thread of the epilogue owns a query row (TMEM lane) and half of a chunk's
 // slots; the sums over rows run across lanes (a butterfly that halves the
 // columns as it halves the rows) and then across the four warps of a half, in
