@@ -99,10 +99,16 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / CS;
+  // a cluster barrier takes 1300 cycles even for one CTA
+  auto meet = [&]() {
+    if (CS > 1) cluster.sync();
+    else __syncthreads();
+  };
 
   grid_dependency_wait();  // acc and lens come from the previous kernel
   allow_dependents_launch();
   const int32_t L = a.lens[b];
+  const int64_t protect_from = a.recent > 0 ? (int64_t)a.end_pos[b] - a.recent : 0;
   const bool bad = L < 0 || (int64_t)L > a.ld;
   const int32_t n = min(L, a.budget);
   int32_t* const dst = a.dst + (int64_t)b * a.ld_moves;
@@ -126,7 +132,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   const int s_lo = min(rank * S, L), m = min(s_lo + S, L) - s_lo;  // this CTA's slots
   const float* const acc = a.acc + (int64_t)b * a.ld + s_lo;
   const int32_t* const pos = a.recent > 0 ? a.pos + (int64_t)b * a.ld + s_lo : nullptr;
-  const int64_t protect_from = a.recent > 0 ? (int64_t)a.end_pos[b] - a.recent : 0;
   auto make_key = [&](int i) { return slot_key(acc[i], pos && pos[i] >= protect_from); };
 
   for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
         count4(sm.hist[pass], bin, on);
       }
     }
-    cluster.sync();
+    meet();
     for (int i = threadIdx.x; i < bins; i += kThreads) {
       uint32_t v = 0;
       for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(&sm.hist[pass][0], q)[i];
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     sm.cnt[0] = free_all;
     sm.cnt[1] = surv_all;
   }
-  cluster.sync();
+  meet();
   if (warp == 0) {
     const uint32_t f = lane < CS ? cluster.map_shared_rank(&sm.cnt[0], lane)[0] : 0u;
     const uint32_t s = lane < rank ? cluster.map_shared_rank(&sm.cnt[0], lane)[1] : 0u;
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
       sm.base[1] = s_before;
     }
   }
-  cluster.sync();  // also: no CTA leaves while another reads its counts
+  meet();  // also: no CTA leaves while another reads its counts
   const uint32_t moves = sm.total;
   if ((int64_t)moves > a.ld_moves) {
     if (rank == 0 && threadIdx.x == 0) {
