@@ -35,12 +35,12 @@ constexpr int kSmemMax = 227 * 1024;
 
 struct alignas(16) PlanSmem {
   uint32_t hist[3][kBins];  // one per pass: no CTA clears what another still reads
-  uint32_t tot[kBins];      // cluster-wide counts of the current pass
+  uint32_t warp_sum[3][kWarps];  // cluster-wide counts of each warp's bins, per pass
   alignas(16) uint64_t warp_tot[32];
   uint32_t cnt[2];          // this CTA's free slots below n, survivors from n on
   uint32_t base[2];         // those of the CTAs before it
   uint32_t total;           // moves of the sequence
-  uint32_t digit, remaining, eq_before;
+  uint32_t digit, remaining, eq_before, bin_count;
 };
 
 static_assert((int64_t)sizeof(PlanSmem) + 8 * (DSA_MAX_PLAN_SLOTS / kMaxCS / 32 + 4) <= kSmemMax, "shared memory");
@@ -220,38 +220,49 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
       }
     }
     meet();
-    for (int i = threadIdx.x; i < bins; i += kThreads) {
-      uint32_t v = 0;
-      for (int q = 0; q < CS; ++q) v += cluster.map_shared_rank(&sm.hist[pass][0], q)[i];
-      sm.tot[i] = v;
+    // The bin, from the top, that holds the remaining-th largest key: lane l of
+    // warp w has the bins bins-1 - 64 w - 2 l and the one below, summed over the
+    // cluster.  The warps' sums say which warp has it, and that one looks
+    // inside.
+    const int hi = bins - 1 - 64 * warp - 2 * lane;
+    uint32_t c0 = 0, c1 = 0;
+    if (hi > 0) {
+      for (int q = 0; q < CS; ++q) {
+        const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[pass][0], q) + hi - 1);
+        c0 += v.y;
+        c1 += v.x;
+      }
     }
+    const uint32_t mine = __reduce_add_sync(0xffffffffu, c0 + c1);
+    if (lane == 0) sm.warp_sum[pass][warp] = mine;
     __syncthreads();
-    // the bin, from the top, that holds the remaining-th largest key: thread
-    // t takes the kPer bins from bins-1 - kPer t downwards
-    constexpr int kPer = kBins / kThreads;
-    const int hi = bins - 1 - kPer * (int)threadIdx.x;
-    uint32_t c[kPer], mine = 0;
+    const uint32_t t = sm.warp_sum[pass][lane];
+    uint32_t inc = t;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      c[e] = hi - e >= 0 ? sm.tot[hi - e] : 0u;
-      mine += c[e];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
     }
-    uint64_t all;
-    uint32_t above = (uint32_t)scan_excl(mine, sm, &all);
+    uint32_t above = __shfl_sync(0xffffffffu, inc - t, warp);
     if (above < remaining && remaining <= above + mine) {
+      inc = c0 + c1;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (above < remaining && remaining <= above + c[e]) {
-          sm.digit = (uint32_t)(hi - e);
-          sm.remaining = remaining - above;
-        }
-        above += c[e];
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      above += inc - (c0 + c1);
+      if (above < remaining && remaining <= above + c0 + c1) {
+        const bool second = remaining > above + c0;
+        sm.digit = (uint32_t)(second ? hi - 1 : hi);
+        sm.remaining = remaining - above - (second ? c0 : 0u);
+        sm.bin_count = second ? c1 : c0;
       }
     }
     __syncthreads();
     prefix |= sm.digit << shift;
     remaining = sm.remaining;
-    __syncthreads();
+    if (pass < 2) __syncthreads();  // read before the next pass writes them
   }
   const uint32_t tau = prefix, need_eq = remaining;
   if (warp == 0) {  // keys equal to tau in the CTAs before this one
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   __syncthreads();
   const int w_lo = min((int)threadIdx.x * wpt, words), w_hi = min(w_lo + wpt, words);
   uint32_t eq_rank = 0;
-  const bool all_eq = sm.tot[tau & 1023u] == need_eq;  // every key equal to tau stays: no ranks are needed
+  const bool all_eq = sm.bin_count == need_eq;  // every key equal to tau stays: no ranks are needed
   if (!all_eq) {
     uint32_t eqs = 0;
     uint64_t unused;
