@@ -6,15 +6,12 @@
 // With 128 heads a slot costs 2 * 128 * (576 + 512) flops and 1152 bytes: 242
 // flops per byte, the ratio of this card's measured rates, so the kernel has
 // to keep the tensor cores and the memory busy at the same time.  With fewer
-// heads the memory bounds it.
+// heads the memory bounds it; tiles of up to 32 (token, head) rows go to
+// paged_mla_few.cu.
 //
-// Split.  The rows' 128-slot chunks form one list; every cluster of two CTAs
-// takes an equal, contiguous part of it, whatever the sequences' lengths
-// (they are read on the device).  A row that lies in one cluster's part is
-// finished there; a row cut by part boundaries leaves one partial per
-// cluster, joined by paged_mla_combine_kernel.  At most two partials per
-// cluster exist (the row that begins before its part, the row that goes on
-// behind it).
+// Split.  Every cluster of two CTAs is a worker with an equal part of all
+// tiles' 128-slot chunks (paged_mla.cuh); paged_mla_combine_kernel joins the
+// tiles that part boundaries cut.
 //
 // Two CTAs.  A 128-head tile's output fills an SM's tensor memory (128 lanes x
 // 512 fp32 columns), so the pair divides the work by role:
@@ -55,9 +52,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <algorithm>
-
-#include "paged.cuh"
+#include "paged_mla.cuh"
 #include "tmap.h"
 
 namespace dsa {
@@ -120,9 +115,8 @@ enum Bar : int {
 };
 constexpr int kMiscOff = kBarOff + kNumBar * 8;
 struct Misc {
-  int tmem_base, abort, first_row, pad;
-  int64_t first_unit, total_units, share;
-  int64_t warp_sum[kThreads / 32];
+  int tmem_base, abort;
+  MlaScan<kThreads> scan;
 };
 constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -131,76 +125,6 @@ constexpr int kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // CTA 0: query blocks 0-7 in [0, 256), S buffers at 256 and 384
 constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
-
-// A row that part boundaries cut, as the combine kernel sees it.
-struct CutRow {
-  int q0;     // first row of out; -1: none
-  int first;  // cluster of its first partial
-  int count;  // partials, one per cluster from `first` on
-  int m;      // rows
-};
-
-struct PagedMlaParams {
-  PagePool pool;
-  const int32_t* lens;
-  int T, H, n_clusters;
-  int tp;            // tokens per tile: as many as 128 rows (token, head) hold
-  int tiles;         // tiles per sequence
-  int n_rows;        // B * tiles
-  int box;           // rows per TMA box
-  float scale_log2;
-  void* out;
-  int out_bf16;
-  float* lse;
-  CutRow* cut;       // [n_clusters]
-  float* part_ml;    // [2 * n_clusters][2][tp * H]: maximum, sum
-  float* part_sc;    // [2 * n_clusters][16][tp * H]: what 32 columns are to be multiplied by
-  uint4* part_o;     // [2 * n_clusters][64][tp * H][8] fp16, unnormalised
-  int32_t* status;
-  int debug_stall;
-  uint64_t wait_limit_ns;
-};
-
-// Slots that the last token of tile r sees.
-__device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool& bad) {
-  const int b = r / p.tiles, t1 = min(p.T, (r - b * p.tiles + 1) * p.tp);
-  const int32_t len = checked_len(__ldg(p.lens + b), pool_capacity(p.pool), bad);
-  return max(0, len - p.T + t1);
-}
-__device__ __forceinline__ int64_t n_chunks_of(int32_t len) { return ((int64_t)len + kChunk - 1) / kChunk; }
-
-// One after the other, the parts of tiles that fall to this cluster.  Every
-// role of both CTAs walks the same list.
-struct Walk {
-  int64_t u;       // first unit of row r
-  int64_t w0, w1;  // this cluster's units
-  int r, n_rows;
-  // of the current part:
-  int seq, lo, hi, chunks;
-  int q0, nt, m;  // first row of q and out, tokens, rows (token, head)
-  int32_t len;    // slots the tile's last token sees
-  bool bad;
-
-  __device__ __forceinline__ bool next(const PagedMlaParams& p) {
-    while (r < n_rows && u < w1) {
-      len = row_len(p, r, bad);
-      const int64_t c = n_chunks_of(len), u0 = u + kRowUnits;
-      seq = r / p.tiles;
-      const int t0 = (r - seq * p.tiles) * p.tp;
-      q0 = (seq * p.T + t0) * p.H;
-      nt = min(p.tp, p.T - t0);
-      m = nt * p.H;
-      chunks = (int)c;
-      const bool starts_here = u >= w0;
-      lo = (int)min(max(w0 - u0, (int64_t)0), c);
-      hi = (int)min(max(w1 - u0, (int64_t)0), c);
-      ++r;
-      u = u0 + c;
-      if (lo < hi || (c == 0 && starts_here)) return true;
-    }
-    return false;
-  }
-};
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -263,77 +187,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dependency_wait();    // lens, q and the cache may come from the previous kernel
   allow_dependents_launch();
 
-  // ---- the units of all rows, and the row this cluster's part begins in
   const int cl = blockIdx.x >> 1;
-  {
-    const int per = (p.n_rows + kThreads - 1) / kThreads;
-    const int r0 = min((int)threadIdx.x * per, p.n_rows), r1 = min(r0 + per, p.n_rows);
-    int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) {
-      bool bad;
-      mine += kRowUnits + n_chunks_of(row_len(p, r, bad));
-    }
-    int64_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) misc->warp_sum[warp] = inc;
-    __syncthreads();
-    // every warp adds the warps' sums up for itself
-    int64_t total = lane < kThreads / 32 ? misc->warp_sum[lane] : 0, before = lane < warp ? total : 0;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    before += inc - mine;
-    const int64_t share = ceil_div(total, p.n_clusters), w0 = share * cl;
-    if (threadIdx.x == 0) {
-      misc->total_units = total;
-      misc->share = share;
-      if (w0 >= total) misc->first_row = p.n_rows;
-    }
-    if (before <= w0 && w0 < before + mine) {  // one thread, if any
-      int64_t u = before;
-      for (int r = r0; r < r1; ++r) {
-        bool bad;
-        const int64_t c = n_chunks_of(row_len(p, r, bad));
-        if (w0 < u + kRowUnits + c) {
-          misc->first_row = r;
-          misc->first_unit = u;
-          break;
-        }
-        u += kRowUnits + c;
-      }
-    }
-  }
-  __syncthreads();
+  auto wk = first_part<kChunk, kRowUnits, kThreads>(p, cl, &misc->scan);
   const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
-  const int64_t share = misc->share;
-  Walk wk;
-  wk.w0 = share * cl;
-  wk.w1 = min(wk.w0 + share, misc->total_units);
-  wk.r = misc->first_row;
-  wk.n_rows = p.n_rows;
-  wk.u = wk.r < p.n_rows ? misc->first_unit : 0;
-
-  if (rank == 1 && threadIdx.x == kSendWarp * 32) {
-    // this cluster's boundary cuts a row: the boundary behind the row's first
-    // partial describes the row to the combine kernel
-    CutRow c{-1, 0, 0, 0};
-    Walk first = wk;
-    const int64_t u0 = wk.u + kRowUnits;
-    if (first.next(p) && wk.w0 > u0 && wk.w0 - share <= u0) {
-      c.q0 = first.q0;
-      c.first = cl - 1;
-      const int64_t last = u0 + first.chunks - 1 - share * c.first;
-      c.count = (int)ceil_div(last + 1, (int)min(share, (int64_t)INT32_MAX));
-      c.m = first.m;
-    }
-    p.cut[cl] = c;
-  }
+  if (rank == 1 && threadIdx.x == kSendWarp * 32) p.cut[cl] = wk.cut_row(p, cl);
   cluster_wait_acquire();
   const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const int nbox64 = kSub / p.box;  // boxes per 64 slots
@@ -916,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   if (v < INFINITY) big = fmaxf(big, v);
                 }
               }
-              const int e = min(max((int)(__float_as_uint(big) >> 23), 1), 253);  // biased exponent
+              const int e = partial_exponent(big);
               const float scale = __uint_as_float((uint32_t)(254 - e) << 23);
               p.part_sc[(part * (kDV / 32) + c0 / 32) * pm + h] = __uint_as_float((uint32_t)e << 23);  // 1 / scale
 #pragma unroll
@@ -990,16 +847,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // thread instead of 64 one behind the other), with many rows it is the other
 // way round.
 constexpr int kCombineWarps = 8;
-constexpr int kMaxClusters = 128;
+constexpr int kMaxWorkers = 256;
 
 template <int SPLIT>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
-                             const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_clusters, int pm,
+                             const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_workers, int pm,
                              void* out, int out_bf16, float* lse) {
   constexpr int kGroups = kCombineWarps / SPLIT;  // column groups per task
   constexpr int kFlight = 8;                       // partials a thread has in flight
-  __shared__ CutRow s_cut[kMaxClusters];
+  __shared__ CutRow s_cut[kMaxWorkers];
   __shared__ int s_n;
   __shared__ float s_sum[SPLIT > 1 ? kCombineWarps : 1][10][32];
   grid_dependency_wait();
@@ -1007,9 +864,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     int n = 0;
-    for (int c0 = 0; c0 < n_clusters; c0 += 32) {
+    for (int c0 = 0; c0 < n_workers; c0 += 32) {
       CutRow c{-1, 0, 0, 0};
-      if (c0 + lane < n_clusters) c = cut[c0 + lane];
+      if (c0 + lane < n_workers) c = cut[c0 + lane];
       const uint32_t m = __ballot_sync(0xffffffffu, c.q0 >= 0);
       if (c.q0 >= 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = c;
       n += __popc(m);
@@ -1118,7 +975,7 @@ int paged_clusters() {
   static int count[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  const int half = std::max(1, std::min(device_info().sm_count / 2, kMaxClusters));
+  const int half = std::max(1, std::min(device_info().sm_count / 2, kMaxWorkers));
   if (dev < 0 || dev >= 64) return half;
   const cudaError_t e = once.run([&] {
     cudaError_t e2 = cudaFuncSetAttribute(paged_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
@@ -1146,8 +1003,14 @@ int paged_clusters() {
 // Tokens whose (token, head) rows fit in one tile.
 int tokens_per_tile(int T, int H) { return std::max(1, std::min(T, 128 / H)); }
 
+// Tiles of up to 32 rows have a kernel of their own, one CTA per worker (128
+// sequences of 500 to 4000 slots: 16 heads 74 us, 92 with the pair; 32 heads
+// 82, 94; with 64 heads it took 109, the pair 100).
+bool few_rows(int T, int H) { return tokens_per_tile(T, H) * H <= kFewRows; }
+int paged_workers(int T, int H) { return few_rows(T, H) ? paged_few_workers() : paged_clusters(); }
+
 size_t paged_workspace(int T, int H) {
-  const size_t n = (size_t)paged_clusters(), m = (size_t)tokens_per_tile(T, H) * H;
+  const size_t n = (size_t)paged_workers(T, H), m = (size_t)tokens_per_tile(T, H) * H;
   return n * sizeof(CutRow) + 2 * n * m * kDV * sizeof(__half) + 2 * n * m * (2 + kDV / 32) * sizeof(float);
 }
 
@@ -1175,7 +1038,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if (!workspace || ws_bytes < need || !is_aligned16(workspace)) return DSA_ERR_WORKSPACE;
   MlaParams debug;
   take_attention_debug(debug);
-  const int n = paged_clusters();
+  const int n = paged_workers(T, H);
   PagedMlaParams p;
   p.pool = PagePool{page_table, ld_table, n_pages, max_pages, page_size};
   p.lens = lens;
@@ -1184,7 +1047,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.tp = tokens_per_tile(T, H);
   p.tiles = (T + p.tp - 1) / p.tp;
   p.n_rows = B * p.tiles;
-  p.n_clusters = n;
+  p.n_workers = n;
   p.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
@@ -1198,23 +1061,27 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
   p.wait_limit_ns = debug.wait_limit_ns;
-  CUtensorMap tq, tk, tv;
-  const uint64_t rows = (uint64_t)n_pages * page_size;
-  bool maps = make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
-                           CU_TENSOR_MAP_SWIZZLE_128B) &&
-              make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, rows, kDQK * 2, 64, (uint32_t)p.box,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
-  tv = tk;
-  if (p.box == 64) {  // a tile of V is one box: 64 rows of four column blocks
-    const uint64_t dims[3] = {64, rows, kKB}, strides[2] = {kDQK * 2, 128};
-    const uint32_t box_v[3] = {64, 64, 4};
-    maps = maps &&
-           make_tmap_3d(&tv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_v, CU_TENSOR_MAP_SWIZZLE_128B);
-  }
-  if (!maps) return DSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  const uint64_t rows = (uint64_t)n_pages * page_size;
+  if (few_rows(T, H)) {
+    if (launch_paged_mla_few(p, q, (uint64_t)B * T * H, kv_pages, rows, s) != cudaSuccess) return DSA_ERR_CUDA;
+  } else {
+    CUtensorMap tq, tk, tv;
+    bool maps = make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, 128,
+                             CU_TENSOR_MAP_SWIZZLE_128B) &&
+                make_tmap_2d(&tk, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, rows, kDQK * 2, 64, (uint32_t)p.box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+    tv = tk;
+    if (p.box == 64) {  // a tile of V is one box: 64 rows of four column blocks
+      const uint64_t dims[3] = {64, rows, kKB}, strides[2] = {kDQK * 2, 128};
+      const uint32_t box_v[3] = {64, 64, 4};
+      maps = maps &&
+             make_tmap_3d(&tv, kv_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box_v, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (!maps) return DSA_ERR_CUDA;
+    if (launch_pdl(paged_mla_kernel, dim3(2 * (unsigned)n), dim3(kThreads), kSmemBytes, s, tq, tk, tv, p) != cudaSuccess)
+      return DSA_ERR_CUDA;
+  }
   if (n > 1) {
     // Warps that share a row's partials, by how many a row has at most (one
     // row of 32K: 30.9 us with eight, 33.0 with four, 37.0 with two; two rows

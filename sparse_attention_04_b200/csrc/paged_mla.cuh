@@ -1,0 +1,189 @@
+// paged_mla.cuh -- what the two kernels for attention over a paged cache
+// share: the launch's parameters, the division of the work, and the partials
+// that the joining kernel reads.
+//
+// A tile is as many tokens of a sequence as fit 128 (token, head) rows; its
+// slots are read in chunks.  The tiles' units (their chunks, and a few for
+// what a tile costs besides) form one list; every worker (a CTA, or a pair)
+// takes an equal, contiguous part of it, whatever the sequences' lengths (they
+// are read on the device).  A tile that lies in one worker's part is finished
+// there; a tile cut by part boundaries leaves one partial per worker.  A worker
+// has at most two partials: the tile that begins before its part, and the tile
+// that goes on behind it.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace dsa {
+
+// A tile that part boundaries cut, as the joining kernel sees it.
+struct CutRow {
+  int q0;     // first row of out; -1: none
+  int first;  // worker of its first partial
+  int count;  // partials, one per worker from `first` on
+  int m;      // rows
+};
+
+struct PagedMlaParams {
+  PagePool pool;
+  const int32_t* lens;
+  int T, H, n_workers;
+  int tp;            // tokens per tile
+  int tiles;         // tiles per sequence
+  int n_rows;        // B * tiles
+  int box;           // rows per TMA box
+  float scale_log2;
+  void* out;
+  int out_bf16;
+  float* lse;
+  CutRow* cut;       // [n_workers]
+  float* part_ml;    // [2 * n_workers][2][tp * H]: maximum, sum
+  float* part_sc;    // [2 * n_workers][16][tp * H]: what 32 columns are to be multiplied by
+  uint4* part_o;     // [2 * n_workers][64][tp * H][8] fp16, unnormalised
+  int32_t* status;
+  int debug_stall;
+  uint64_t wait_limit_ns;
+};
+
+// Slots that the last token of tile r sees.
+__device__ __forceinline__ int32_t row_len(const PagedMlaParams& p, int r, bool& bad) {
+  const int b = r / p.tiles, t1 = min(p.T, (r - b * p.tiles + 1) * p.tp);
+  const int32_t len = checked_len(__ldg(p.lens + b), pool_capacity(p.pool), bad);
+  return max(0, len - p.T + t1);
+}
+
+// One after the other, the parts of tiles that fall to this worker.  Every
+// role walks the same list.  CHUNK: slots per chunk; UNITS: what a tile costs
+// besides its chunks, in chunks.
+template <int CHUNK, int UNITS>
+struct MlaWalk {
+  int64_t u;       // first unit of tile r
+  int64_t w0, w1;  // this worker's units
+  int64_t share;   // units per worker
+  int r, n_rows;
+  // of the current part:
+  int seq, lo, hi, chunks;
+  int q0, nt, m;  // first row of q and out, tokens, rows (token, head)
+  int32_t len;    // slots the tile's last token sees
+  bool bad;
+
+  static __device__ __forceinline__ int64_t chunks_of(int32_t len) { return ((int64_t)len + CHUNK - 1) / CHUNK; }
+
+  __device__ __forceinline__ bool next(const PagedMlaParams& p) {
+    while (r < n_rows && u < w1) {
+      len = row_len(p, r, bad);
+      const int64_t c = chunks_of(len), u0 = u + UNITS;
+      seq = r / p.tiles;
+      const int t0 = (r - seq * p.tiles) * p.tp;
+      q0 = (seq * p.T + t0) * p.H;
+      nt = min(p.tp, p.T - t0);
+      m = nt * p.H;
+      chunks = (int)c;
+      const bool starts_here = u >= w0;
+      lo = (int)min(max(w0 - u0, (int64_t)0), c);
+      hi = (int)min(max(w1 - u0, (int64_t)0), c);
+      ++r;
+      u = u0 + c;
+      if (lo < hi || (c == 0 && starts_here)) return true;
+    }
+    return false;
+  }
+
+  // The tile that this worker's first boundary cuts, if its first partial ends
+  // there: that boundary describes the tile to the joining kernel.
+  __device__ __forceinline__ CutRow cut_row(const PagedMlaParams& p, int worker) const {
+    CutRow c{-1, 0, 0, 0};
+    MlaWalk first = *this;
+    const int64_t u0 = u + UNITS;
+    if (first.next(p) && w0 > u0 && w0 - share <= u0) {
+      c.q0 = first.q0;
+      c.first = worker - 1;
+      const int64_t last = u0 + first.chunks - 1 - share * c.first;
+      c.count = (int)ceil_div(last + 1, (int)min(share, (int64_t)INT32_MAX));
+      c.m = first.m;
+    }
+    return c;
+  }
+};
+
+// The units of all tiles, and the tile a worker's part begins in.  By all
+// THREADS threads of a CTA, which meet on the way; sh needs no values before.
+template <int THREADS>
+struct MlaScan {
+  int64_t first_unit, total_units, share, warp_sum[THREADS / 32];
+  int first_row, pad;
+};
+template <int CHUNK, int UNITS, int THREADS>
+__device__ __forceinline__ MlaWalk<CHUNK, UNITS> first_part(const PagedMlaParams& p, int worker, MlaScan<THREADS>* sh) {
+  using Walk = MlaWalk<CHUNK, UNITS>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.n_rows + THREADS - 1) / THREADS;
+  const int r0 = min((int)threadIdx.x * per, p.n_rows), r1 = min(r0 + per, p.n_rows);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    mine += UNITS + Walk::chunks_of(row_len(p, r, bad));
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh->warp_sum[warp] = inc;
+  __syncthreads();
+  // every warp adds the warps' sums up for itself
+  int64_t total = lane < THREADS / 32 ? sh->warp_sum[lane] : 0, before = lane < warp ? total : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  before += inc - mine;
+  const int64_t share = ceil_div(total, p.n_workers), w0 = share * worker;
+  if (threadIdx.x == 0) {
+    sh->total_units = total;
+    sh->share = share;
+    if (w0 >= total) sh->first_row = p.n_rows;
+  }
+  if (before <= w0 && w0 < before + mine) {  // one thread, if any
+    int64_t u = before;
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      const int64_t c = Walk::chunks_of(row_len(p, r, bad));
+      if (w0 < u + UNITS + c) {
+        sh->first_row = r;
+        sh->first_unit = u;
+        break;
+      }
+      u += UNITS + c;
+    }
+  }
+  __syncthreads();
+  Walk wk;
+  wk.share = sh->share;
+  wk.w0 = wk.share * worker;
+  wk.w1 = min(wk.w0 + wk.share, sh->total_units);
+  wk.r = sh->first_row;
+  wk.n_rows = p.n_rows;
+  wk.u = wk.r < p.n_rows ? sh->first_unit : 0;
+  return wk;
+}
+
+// The scale of a partial's 32 columns: the biased exponent of the largest
+// finite one, so that the largest comes to [1, 2).
+__device__ __forceinline__ int partial_exponent(float big) {
+  return min(max((int)(__float_as_uint(big) >> 23), 1), 253);
+}
+
+// The kernel for tiles of up to kFewRows rows, one CTA per worker.
+constexpr int kFewRows = 32;
+int paged_few_workers();  // workers of a launch: a CTA per SM
+cudaError_t launch_paged_mla_few(const PagedMlaParams& p, const void* q, uint64_t q_rows, const void* kv_pages,
+                                 uint64_t pool_rows, cudaStream_t s);
+
+}  // namespace dsa

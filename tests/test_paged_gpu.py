@@ -128,7 +128,7 @@ LENS = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256,
 
 
 @pytest.mark.parametrize("P", [16, 48, 64, 80, 128, 256])
-@pytest.mark.parametrize("H", [1, 16, 100, 128])
+@pytest.mark.parametrize("H", [1, 16, 27, 32, 33, 100, 128])
 def test_attention_at_every_edge_of_pages_and_tiles(cuda_device, P, H):
     c = Cache(cuda_device, LENS, P, seed=P + H)
     q = _q(c, len(LENS), 1, H)
@@ -137,7 +137,7 @@ def test_attention_at_every_edge_of_pages_and_tiles(cuda_device, P, H):
     _check_attention(c, q, out, lse)
 
 
-@pytest.mark.parametrize("H", [7, 64, 128])
+@pytest.mark.parametrize("H", [1, 6, 7, 16, 64, 128])
 @pytest.mark.parametrize("T", [2, 5])
 def test_attention_of_several_new_tokens_is_causal(cuda_device, T, H):
     lens = [0, 1, T - 1, T, T + 1, 64, 66, 130, 777]
@@ -164,7 +164,8 @@ def test_attention_of_several_new_tokens_is_causal(cuda_device, T, H):
 
 
 @pytest.mark.parametrize("lens,H,T", [([40000], 128, 1), ([33000, 5, 0, 70001, 12345], 128, 1), ([9999] * 3, 128, 2),
-                                      ([50021, 3, 800], 16, 1), ([20000] * 9, 40, 3)])
+                                      ([50021, 3, 800], 16, 1), ([20000] * 9, 40, 3), ([40000], 8, 3),
+                                      ([33000, 5, 0, 70001, 12345], 16, 2), ([9999] * 150, 32, 1)])
 def test_attention_of_long_rows_split_and_joined(cuda_device, lens, H, T):
     c = Cache(cuda_device, lens, 64, seed=len(lens))
     q = _q(c, len(lens), T, H)
@@ -175,30 +176,33 @@ def test_attention_of_long_rows_split_and_joined(cuda_device, lens, H, T):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
-def test_attention_of_many_short_rows(cuda_device):
+@pytest.mark.parametrize("H", [128, 20, 5])
+def test_attention_of_many_short_rows(cuda_device, H):
     g = torch.Generator().manual_seed(3)
     lens = torch.randint(0, 400, (300,), generator=g).tolist()
     c = Cache(cuda_device, lens, 16, seed=1)
-    q = _q(c, len(lens), 1, 128)
+    q = _q(c, len(lens), 1, H)
     out, lse, st = _attend(c, q)
     assert st == 0
     _check_attention(c, q, out, lse)
 
 
-def test_attention_in_fp32_and_with_other_scales(cuda_device):
+@pytest.mark.parametrize("H", [128, 9])
+def test_attention_in_fp32_and_with_other_scales(cuda_device, H):
     lens = [1, 100, 3001]
     c = Cache(cuda_device, lens, 64, seed=5)
     for scale, mul in ((SCALE, 1.0), (-SCALE, 1.0), (0.0, 1.0), (1.0, 1.0), (SCALE, 30.0)):
-        q = _q(c, 3, 1, 128, mul)
+        q = _q(c, 3, 1, H, mul)
         out, lse, st = _attend(c, q, torch.float32, scale)
         assert st == 0
         _check_attention(c, q, out, lse, scale)
 
 
-def test_attention_follows_a_rising_maximum(cuda_device):
+@pytest.mark.parametrize("H", [128, 12, 32])
+def test_attention_follows_a_rising_maximum(cuda_device, H):
     """Keys in order of growing logits: the running maximum moves in every tile."""
     c = Cache(cuda_device, [2000], 64, seed=6)
-    q = _q(c, 1, 1, 128)
+    q = _q(c, 1, 1, H)
     direction = q[0, 0].double().mean(0)
     k = torch.randn(2000, D, generator=c.g, device=c.dev, dtype=torch.float64) * 0.1
     k += torch.linspace(-60, 60, 2000, device=c.dev)[:, None] * direction / direction.norm()
@@ -210,7 +214,8 @@ def test_attention_follows_a_rising_maximum(cuda_device):
         _check_attention(c, qq, out, lse, 1.0)
 
 
-def test_attention_beyond_32_bit_offsets(cuda_device):
+@pytest.mark.parametrize("H", [128, 16])
+def test_attention_beyond_32_bit_offsets(cuda_device, H):
     """A pool of 4.6 G elements, the sequence on its last pages."""
     P, n = 64, 125000
     c = Cache(cuda_device, [1500], P, seed=7)
@@ -219,7 +224,7 @@ def test_attention_beyond_32_bit_offsets(cuda_device):
     table = torch.arange(n - pages, n, dtype=torch.int32, device=c.dev)[None].contiguous()
     kv[table[0].long()] = c.kv[c.table[0].long()]
     c.kv, c.table = kv, table
-    q = _q(c, 1, 1, 128)
+    q = _q(c, 1, 1, H)
     out, lse, st = _attend(c, q)
     assert st == 0
     _check_attention(c, q, out, lse)
@@ -227,7 +232,8 @@ def test_attention_beyond_32_bit_offsets(cuda_device):
     _check_weights(c, q, lse, acc, 1.0)
 
 
-def test_attention_takes_a_bad_page_as_masked(cuda_device):
+@pytest.mark.parametrize("H", [128, 16])
+def test_attention_takes_a_bad_page_as_masked(cuda_device, H):
     lens = [300, 300, 64, 5000]
     c = Cache(cuda_device, lens, 64, seed=8)
     bad = {0: [1], 2: [0], 3: [0, 40, 78]}
@@ -241,7 +247,7 @@ def test_attention_takes_a_bad_page_as_masked(cuda_device):
             s[64 * i:64 * i + 64] = True
         return s
 
-    q = _q(c, 4, 1, 128)
+    q = _q(c, 4, 1, H)
     out, lse, st = _attend(c, q)
     assert st == 6  # DSA_ERR_BAD_INDEX
     c.table.clamp_(0, c.kv.shape[0] - 1)  # for the reference: any page, its slots are skipped
@@ -326,7 +332,7 @@ def test_attention_with_nothing_but_padding_and_with_more_sequences_than_cluster
     assert torch.equal(out[ones], rows.expand(-1, 1, 16, -1))
 
 
-@pytest.mark.parametrize("H,T", [(128, 1), (16, 4)])
+@pytest.mark.parametrize("H,T", [(128, 1), (16, 4), (16, 2), (3, 1)])
 def test_attention_over_infinities_and_huge_values(cuda_device, H, T):
     """Values near the type's largest in the cache, infinities in slots behind the
     end; nothing overflows on the way (partials are scaled)."""
@@ -726,12 +732,13 @@ def test_cache_object_runs_the_same_calls(cuda_device):
     assert lens.tolist() == [36, 36] and int(one.status.item()) == 0
 
 
-def test_attention_wait_runs_out_then_next_call_is_correct(cuda_device):
+@pytest.mark.parametrize("H", [128, 16])
+def test_attention_wait_runs_out_then_next_call_is_correct(cuda_device, H):
     """The timeout path (test hook): a bounded wait that never comes true ends the
     launch with DSA_ERR_TIMEOUT, and the launch after it is right."""
     L = _lib()
     c = Cache(cuda_device, [3000, 40, 0, 700], 64, seed=40)
-    q = _q(c, 4, 1, 128)
+    q = _q(c, 4, 1, H)
     L.debug_stall_attention(1, 5_000_000)
     try:
         _, _, st = _attend(c, q)
@@ -743,13 +750,14 @@ def test_attention_wait_runs_out_then_next_call_is_correct(cuda_device):
     _check_attention(c, q, out, lse)
 
 
-def test_two_streams_and_two_graphs_with_a_workspace_each(cuda_device):
+@pytest.mark.parametrize("H", [64, 16])
+def test_two_streams_and_two_graphs_with_a_workspace_each(cuda_device, H):
     """Calls that overlap: the results are those of the calls alone."""
     L = _lib()
     cs = [Cache(cuda_device, lens, 32, seed=50 + i) for i, lens in enumerate(([5000, 300], [77, 9000]))]
-    qs = [_q(c, 2, 1, 64) for c in cs]
+    qs = [_q(c, 2, 1, H) for c in cs]
     want = [_attend(c, q)[:2] for c, q in zip(cs, qs)]
-    n = L.paged_mla_workspace_size(2, 1, 64)
+    n = L.paged_mla_workspace_size(2, 1, H)
     got, graphs, streams = [], [], [torch.cuda.Stream() for _ in cs]
     for c, q, s in zip(cs, qs, streams):
         out, lse, ws = torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), torch.empty(n, dtype=torch.uint8, device=c.dev)
