@@ -21,7 +21,7 @@
 // rescaled only when it rose by more than 2^8.  A row's sum stays per lane
 // until the part ends.
 //
-// What bounds it (B200).  64 sequences, 16 heads, 423 MB of cache: 94 us, 65 of
+// What bounds it (B200).  24 sequences of up to 30K slots (423 MB), two tokens of 16 heads: 94 us, 65 of
 // them the bytes at the measured copy rate (the CTA pair of paged_mla.cu: 117;
 // a ring of eight pieces: 98).  A chunk takes about 3400 cycles, 1350 of them
 // in the consumers; without loads the whole call takes 76.  The rest is latency
