@@ -667,9 +667,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // not finite becomes zeros too (the tokens that see it have a NaN
           // for a sum already).
           const int64_t s0 = (int64_t)i * kSub;
-          const int z_end = (int)min((int64_t)kSub, max((int64_t)0, ((int64_t)wk.len + p.box - 1) / p.box * p.box - s0));
-          const int z_begin = (int)min((int64_t)kSub, max((int64_t)0, (int64_t)wk.len - (wk.nt - 1) - s0));
-          if (z_begin < z_end) {
+          if (s0 + kSub > wk.len - (wk.nt - 1)) {
+            const int z_begin = (int)max((int64_t)0, wk.len - (wk.nt - 1) - s0);
+            const int z_end = (int)min((int64_t)kSub, (((int64_t)wk.len + p.box - 1) & -(int64_t)p.box) - s0);
             const uint32_t k0 = (2 * j) % kVSlots, k1 = (2 * j + 1) % kVSlots;
             ok = warp_wait(bar(kVFull + k0), ((2 * j) / kVSlots) & 1, abort, p.wait_limit_ns) &&
                  warp_wait(bar(kVFull + k1), ((2 * j + 1) / kVSlots) & 1, abort, p.wait_limit_ns);
