@@ -4,8 +4,9 @@
 // Both only move bytes: a token is one 1152-byte row (576 bf16) read and
 // written, plus its acc and pos entries.  HBM bounds them for prompts and
 // large evictions, launch latency for single steps.  B200: 8 prompts of 4096
-// tokens (75.8 MB) in 14.5 us, 98 K moves of random rows (461 MB) in 94 us, 4.9
-// TB/s; four rows in flight per warp instead of one measured the same.
+// tokens (75.8 MB) in 14.5 us, 198 K moves of random rows (461 MB) in 94 us, 4.9
+// TB/s; loads alone of as many rows in flight as registers hold reach 3.6.
+// Four rows in flight per warp instead of one measured the same.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -58,37 +59,66 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One warp per move, the grid's y walks the sequences.
-__global__ void __launch_bounds__(256)
+// One warp per move.  The moves of 256 sequences form one list, dealt out to
+// the warps in turn, because the sequences' lists differ in length and only the
+// device knows them: one list of 16K moves among 32 takes 12 us, 72 with a
+// thirty-second of the card for each sequence.
+constexpr int kMoveThreads = 256, kMoveGroup = kMoveThreads;
+
+__global__ void __launch_bounds__(kMoveThreads)
     paged_move_kernel(__nv_bfloat16* kv, PagePool pool, const int32_t* __restrict__ n_moves,
                       const int32_t* __restrict__ move_dst, const int32_t* __restrict__ move_src, int64_t ld_moves, int B,
                       float* acc, int32_t* pos, int64_t ld_slots, int32_t* status) {
+  __shared__ int64_t s_first[kMoveGroup + 1];  // a sequence's first move in the list
+  __shared__ int64_t s_sum[kMoveThreads / 32];
   grid_dependency_wait();  // the plan may come from the previous kernel
   allow_dependents_launch();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t cap = pool_capacity(pool);
   if (acc || pos) cap = min(cap, ld_slots);
-  for (int b = blockIdx.y; b < B; b += gridDim.y) {
-    const int32_t n = n_moves[b];
+  for (int64_t b0 = (int64_t)blockIdx.y * kMoveGroup; b0 < B; b0 += (int64_t)gridDim.y * kMoveGroup) {
+    int64_t n = b0 + threadIdx.x < B ? n_moves[b0 + threadIdx.x] : 0;
     if (n < 0 || n > ld_moves) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) report(status, DSA_ERR_BAD_OFFSETS);
-      continue;
+      if (blockIdx.x == 0) report(status, DSA_ERR_BAD_OFFSETS);
+      n = 0;
     }
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
-      const int32_t d = move_dst[(int64_t)b * ld_moves + i], s = move_src[(int64_t)b * ld_moves + i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += v;
+    }
+    if (lane == 31) s_sum[warp] = n;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) n += s_sum[w];
+    s_first[threadIdx.x + 1] = n;
+    if (threadIdx.x == 0) s_first[0] = 0;
+    __syncthreads();
+    const int64_t total = s_first[kMoveGroup];
+    const int seqs = (int)min((int64_t)kMoveGroup, B - b0);
+    int at = 0;
+    for (int64_t i = (int64_t)blockIdx.x * (kMoveThreads / 32) + warp; i < total;
+         i += (int64_t)gridDim.x * (kMoveThreads / 32)) {
+      for (int end = seqs; end - at > 1;) {  // s_first[at] <= i < s_first[end]
+        const int mid = (at + end) >> 1;
+        if (s_first[mid] <= i) at = mid;
+        else end = mid;
+      }
+      const int64_t b = b0 + at, m = b * ld_moves + (i - s_first[at]);
+      const int32_t d = move_dst[m], s = move_src[m];
       const bool in = d >= 0 && s >= 0 && d < cap && s < cap;
-      const int64_t rd = in ? pool_row(pool, b, d) : -1, rs = in ? pool_row(pool, b, s) : -1;
+      const int64_t rd = in ? pool_row(pool, (int)b, d) : -1, rs = in ? pool_row(pool, (int)b, s) : -1;
       if (rd < 0 || rs < 0) {
         if (lane == 0) report(status, DSA_ERR_BAD_INDEX);
         continue;
       }
       copy_row(reinterpret_cast<uint4*>(kv + rd * kDQK), reinterpret_cast<const uint4*>(kv + rs * kDQK), lane);
       if (lane == 0) {
-        const int64_t o = (int64_t)b * ld_slots;
+        const int64_t o = b * ld_slots;
         if (acc) acc[o + d] = acc[o + s];
         if (pos) pos[o + d] = pos[o + s];
       }
     }
+    __syncthreads();  // the list is read
   }
 }
 
@@ -125,12 +155,13 @@ int dsa_paged_move(void* kv_pages, const int32_t* page_table, int64_t ld_table, 
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (int rc = check_slots(acc, pos, ld_slots)) return rc;
   const PagePool pool{page_table, ld_table, n_pages, max_pages, page_size};
-  // About eight CTAs of eight warps per SM over all sequences (the lists'
-  // lengths are known on the device only), fewer where the lists are short.
-  const int64_t y = std::min<int64_t>(B, 32768);
-  const int64_t x = std::min<int64_t>((ld_moves + 7) / 8, std::max<int64_t>(1, (8 * (int64_t)device_info().sm_count + y - 1) / y));
+  // Eight CTAs of eight warps per SM over all groups of sequences, fewer where
+  // the lists have no room for as many moves.
+  const int64_t groups = ((int64_t)B + kMoveGroup - 1) / kMoveGroup, y = std::min<int64_t>(groups, 32768);
+  const int64_t room = (std::min<int64_t>(B, kMoveGroup) * ld_moves + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
+  const int64_t x = std::min<int64_t>(room, std::max<int64_t>(1, (8 * (int64_t)device_info().sm_count + y - 1) / y));
   const cudaError_t e =
-      launch_pdl(paged_move_kernel, dim3((unsigned)x, (unsigned)y), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream),
+      launch_pdl(paged_move_kernel, dim3((unsigned)x, (unsigned)y), dim3(kMoveThreads), 0, reinterpret_cast<cudaStream_t>(stream),
                  reinterpret_cast<__nv_bfloat16*>(kv_pages), pool, n_moves, move_dst, move_src, ld_moves, B, acc, pos,
                  ld_slots, dev_status);
   return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;

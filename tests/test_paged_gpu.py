@@ -610,6 +610,42 @@ def test_moves_leave_bad_slots_and_pages_out(cuda_device):
     assert torch.equal(c.kv.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("B", [3, 255, 256, 257, 700])
+def test_moves_of_many_sequences_with_lists_of_every_length(cuda_device, B):
+    """The lists of a group of sequences are dealt out together: none, one, many
+    moves per sequence, one of them long, two with a number of moves that does
+    not fit."""
+    L = _lib()
+    P, cap, ld_moves, ld = 16, 64, 32, 64
+    c = Cache(cuda_device, [cap] * B, P, seed=B)
+    g = torch.Generator().manual_seed(B)
+    n = torch.randint(0, 4, (B,), generator=g)
+    n[torch.randint(0, B, (B // 3,), generator=g)] = 0
+    n[B // 2], n[B - 1] = ld_moves, 1
+    dst = torch.full((B, ld_moves), -9, dtype=torch.int32)
+    src = torch.full((B, ld_moves), -9, dtype=torch.int32)
+    acc = torch.rand(B, ld, generator=g).to(c.dev)
+    pos = torch.randint(0, 99999, (B, ld), generator=g, dtype=torch.int32).to(c.dev)
+    want_kv, want_acc, want_pos = c.kv.clone(), acc.clone(), pos.clone()
+    bad = {0: ld_moves + 1, 1: -1}
+    for b in range(B):
+        k = int(n[b])
+        dst[b, :k] = torch.randperm(32, generator=g)[:k]
+        src[b, :k] = 32 + torch.randperm(32, generator=g)[:k]
+        if b in bad:
+            n[b] = bad[b]
+        elif k:
+            d, s = dst[b, :k].long().to(c.dev), src[b, :k].long().to(c.dev)
+            want_kv.view(-1, D)[c.rows(b, d)] = c.flat[c.rows(b, s)]
+            want_acc[b, d], want_pos[b, d] = acc[b, s], pos[b, s]
+    st = _status(c.dev)
+    L.paged_move(c.kv, c.table, n.int().to(c.dev), dst.to(c.dev), src.to(c.dev), acc=acc, pos=pos, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 7
+    assert torch.equal(c.kv.view(torch.int16), want_kv.view(torch.int16))
+    assert torch.equal(acc, want_acc) and torch.equal(pos, want_pos)
+
+
 # ---------------------------------------------------------------- as a server runs them
 
 @pytest.mark.parametrize("graph", [False, True])
