@@ -14,10 +14,10 @@
 // memory as far as it goes (about 46000 per CTA) and are made again from
 // memory above that.
 //
-// B200: 32 sequences of 64K to 128K slots cut to 64K in 33 us (41 MB: 6.4 us of
-// HBM), eight of 4097 slots in 14 us.  What bounds it is instruction issue and
+// B200: 32 sequences of 64K to 128K slots cut to 64K in 31 us (41 MB: 6.4 us of
+// HBM), eight of 4097 slots in 12 us.  What bounds it is instruction issue and
 // about 30 barrier-separated steps: keys and first histogram 9 us, the digit
-// passes 12, bitmap and ranks 5, lists 6.
+// passes 10, bitmap and ranks 5, lists 6.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
