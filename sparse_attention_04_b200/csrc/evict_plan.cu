@@ -399,6 +399,7 @@ extern "C" int dsa_evict_plan(const float* acc, const int32_t* pos, const int32_
   if (B > (1 << 24)) return DSA_ERR_UNSUPPORTED;
   if (budget < 1 || recent < 0 || recent > budget) return DSA_ERR_INVALID_ARG;
   if (recent > 0 && (!pos || !end_pos)) return DSA_ERR_INVALID_ARG;
+  if (!is_aligned4(lens, end_pos, new_lens, n_moves, move_dst, move_src, dev_status)) return DSA_ERR_INVALID_ARG;
   if (int rc = check_slots(acc, pos, ld_slots)) return rc;
   if (ld_slots > DSA_MAX_PLAN_SLOTS) return DSA_ERR_UNSUPPORTED;
   // CTAs per sequence: one per 8192 slots, up to eight (a portable cluster);

@@ -59,7 +59,10 @@ __device__ __forceinline__ void load_boxes(uint32_t dst, const CUtensorMap* tm, 
 }
 
 inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool is_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+template <class... Ptr>
+bool is_aligned4(Ptr... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
 
 // Checks of the arguments that describe the pool (host).
 inline int check_pool(const void* kv_pages, const int32_t* table, int64_t ld_table, int max_pages, int page_size,

@@ -132,7 +132,8 @@ extern "C" {
 int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* page_table, int64_t ld_table,
                      int max_pages, int B, int T, int page_size, int64_t n_pages, void* kv_pages, float* acc,
                      int32_t* pos, const int32_t* end_pos, int64_t ld_slots, int32_t* dev_status, void* stream) {
-  if (B <= 0 || T <= 0 || !kv_new || !lens || !is_aligned16(kv_new)) return DSA_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || !kv_new || !lens || !is_aligned16(kv_new) || !is_aligned4(lens, end_pos, dev_status))
+    return DSA_ERR_INVALID_ARG;
   if ((int64_t)B * T > (int64_t)1 << 24) return DSA_ERR_UNSUPPORTED;
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (int rc = check_slots(acc, pos, ld_slots)) return rc;
@@ -151,6 +152,7 @@ int dsa_paged_move(void* kv_pages, const int32_t* page_table, int64_t ld_table, 
                    int64_t ld_moves, int B, float* acc, int32_t* pos, int64_t ld_slots, int32_t* dev_status,
                    void* stream) {
   if (B <= 0 || !n_moves || !move_dst || !move_src || ld_moves < 1) return DSA_ERR_INVALID_ARG;
+  if (!is_aligned4(n_moves, move_dst, move_src, dev_status)) return DSA_ERR_INVALID_ARG;
   if (B > (1 << 24)) return DSA_ERR_UNSUPPORTED;
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (int rc = check_slots(acc, pos, ld_slots)) return rc;

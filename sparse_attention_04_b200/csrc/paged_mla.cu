@@ -1033,7 +1033,8 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   if ((int64_t)B * T > (int64_t)1 << 24 || H > DSA_MAX_HEADS) return DSA_ERR_UNSUPPORTED;
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_INVALID_ARG;
-  if (!(scale == scale) || !is_aligned16(q) || !is_aligned16(out)) return DSA_ERR_INVALID_ARG;
+  if (!(scale == scale) || !is_aligned16(q) || !is_aligned16(out) || !is_aligned4(lens, lse, dev_status))
+    return DSA_ERR_INVALID_ARG;
   const size_t need = paged_workspace(T, H);
   if (!workspace || ws_bytes < need || !is_aligned16(workspace)) return DSA_ERR_WORKSPACE;
   MlaParams debug;

@@ -433,7 +433,7 @@ extern "C" int dsa_paged_weights(const void* q, const void* kv_pages, const int3
   if ((int64_t)B * T > (int64_t)1 << 24 || H > DSA_MAX_HEADS) return DSA_ERR_UNSUPPORTED;
   if (int rc = check_pool(kv_pages, page_table, ld_table, max_pages, page_size, n_pages)) return rc;
   if (int rc = check_slots(acc_out, nullptr, ld_slots)) return rc;
-  if (!is_aligned16(acc) || !is_aligned16(q)) return DSA_ERR_INVALID_ARG;
+  if (!is_aligned16(acc) || !is_aligned16(q) || !is_aligned4(lens, lse, dev_status)) return DSA_ERR_INVALID_ARG;
   if (!(scale == scale) || !(decay == decay)) return DSA_ERR_INVALID_ARG;
   PagedWeightsParams p;
   p.pool = PagePool{page_table, ld_table, n_pages, max_pages, page_size};

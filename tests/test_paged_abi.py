@@ -31,7 +31,8 @@ def test_append_refusals(L):
     _refused(L.lib.dsa_paged_append, base, [
         (0, None, 1), (1, None, 1), (2, None, 1), (9, None, 1), (0, P(A + 8), 1), (9, P(A + 2), 1), (2, P(A + 2), 1),
         (3, 7, 1), (4, 0, 1), (5, 0, 1), (6, 0, 1), (5, 1 << 25, 2), (7, 0, 1), (7, 24, 1), (7, -16, 1), (8, 0, 1),
-        (8, 1 << 31, 1), (12, None, 1), (13, 0, 1), (13, 510, 1), (10, P(A + 4), 1), (11, P(A + 4), 1), (13, 1 << 31, 1)])
+        (8, 1 << 31, 1), (12, None, 1), (13, 0, 1), (13, 510, 1), (10, P(A + 4), 1), (11, P(A + 4), 1), (13, 1 << 31, 1),
+        (1, P(A + 2), 1), (12, P(A + 1), 1), (14, P(A + 2), 1)])
 
 
 def test_attention_refusals(L):
@@ -40,7 +41,7 @@ def test_attention_refusals(L):
     _refused(L.lib.dsa_paged_mla, base, [
         (0, None, 1), (1, None, 1), (2, None, 1), (5, None, 1), (12, None, 1), (0, P(A + 2), 1), (1, P(A + 8), 1),
         (12, P(A + 4), 1), (3, 7, 1), (6, 0, 1), (7, -1, 1), (8, 0, 1), (8, 129, 2), (6, (1 << 24) + 1, 2), (9, 8, 1),
-        (9, 65, 1), (10, 0, 1), (10, 1 << 30, 1), (11, float("nan"), 1), (13, 1, 1), (13, 7, 1)])
+        (9, 65, 1), (10, 0, 1), (10, 1 << 30, 1), (11, float("nan"), 1), (13, 1, 1), (13, 7, 1), (5, P(A + 2), 1), (14, P(A + 2), 1), (17, P(A + 3), 1)])
     need = L.paged_mla_workspace_size(2, 1, 128)
     if need:
         _refused(L.lib.dsa_paged_mla, base, [(15, None, 3), (15, P(A + 8), 3), (16, need - 1, 3)])
@@ -53,7 +54,8 @@ def test_weights_refusals(L):
     _refused(L.lib.dsa_paged_weights, base, [
         (0, None, 1), (1, None, 1), (2, None, 1), (5, None, 1), (6, None, 1), (15, None, 1), (0, P(A + 2), 1),
         (14, P(A + 4), 1), (15, P(A + 4), 1), (16, 0, 1), (16, 511, 1), (7, 0, 1), (8, 0, 1), (9, 0, 1), (9, 129, 2),
-        (10, 40, 1), (11, 0, 1), (12, float("nan"), 1), (13, float("nan"), 1)])
+        (10, 40, 1), (11, 0, 1), (12, float("nan"), 1), (13, float("nan"), 1), (5, P(A + 1), 1), (6, P(A + 2), 1),
+        (17, P(A + 2), 1)])
 
 
 def test_plan_refusals(L):
@@ -62,7 +64,8 @@ def test_plan_refusals(L):
     _refused(L.lib.dsa_evict_plan, base, [
         (0, None, 1), (1, None, 1), (2, None, 1), (3, None, 1), (8, None, 1), (9, None, 1), (10, None, 1), (11, None, 1),
         (0, P(A + 4), 1), (1, P(A + 8), 1), (4, 0, 1), (5, 0, 1), (5, 510, 1), (5, (6 << 20) + 4, 2), (6, 0, 1), (7, -1, 1),
-        (7, 101, 1), (12, 0, 1)])
+        (7, 101, 1), (12, 0, 1), (2, P(A + 2), 1), (3, P(A + 2), 1), (8, P(A + 1), 1), (9, P(A + 2), 1), (10, P(A + 2), 1),
+        (11, P(A + 3), 1), (13, P(A + 2), 1)])
 
 
 def test_move_refusals(L):
@@ -70,7 +73,8 @@ def test_move_refusals(L):
     base = [P(A), P(A), 8, 8, 64, 100, P(A), P(A), P(A), 50, 2, P(A), P(A), 512, None, None]
     _refused(L.lib.dsa_paged_move, base, [
         (0, None, 1), (1, None, 1), (6, None, 1), (7, None, 1), (8, None, 1), (2, 7, 1), (3, 0, 1), (4, 50, 1), (5, 0, 1),
-        (9, 0, 1), (10, 0, 1), (11, P(A + 4), 1), (12, P(A + 4), 1), (13, 0, 1), (13, 6, 1), (0, P(A + 4), 1)])
+        (9, 0, 1), (10, 0, 1), (11, P(A + 4), 1), (12, P(A + 4), 1), (13, 0, 1), (13, 6, 1), (0, P(A + 4), 1), (6, P(A + 2), 1), (7, P(A + 2), 1),
+        (8, P(A + 1), 1), (14, P(A + 2), 1)])
 
 
 def test_binding_refuses_tensors_that_do_not_fit(L):
