@@ -181,10 +181,11 @@ class PagedLatentCache:
 
     Lengths, positions and the eviction plan stay on the device, so that the
     whole step can be captured in one CUDA graph.  Every sequence has page
-    lists for `slots` slots; a scheduler that hands pages out writes its own
-    numbers into page_table.  Set lens (and end_pos, the tokens seen so far)
-    after filling the first rows, or append the prompt in calls of T tokens.
-    An append beyond `slots` is left out and reported in status.
+    lists for `slots` slots, rounded up to whole pages; a scheduler that hands
+    pages out writes its own numbers into page_table.  Set lens (and end_pos,
+    the tokens seen so far) after filling the first rows, or append the prompt
+    in calls of T tokens.  A sequence appended to beyond its slots is reported in
+    status and counts as empty until lens is set again.
 
     kv_pages [pages, page_size, 576] bf16, page_table [B, pages per sequence],
     lens and end_pos [B], acc and pos [B, slots] (see include/dsa.h)."""
@@ -193,14 +194,13 @@ class PagedLatentCache:
                  out_dtype=torch.bfloat16, device="cuda"):
         dev = torch.device(device)
         pages = -(-slots // page_size)
-        ld = -(-slots // 4) * 4
-        self.B, self.T, self.H, self.slots = B, T, H, slots
+        self.B, self.T, self.H, self.slots = B, T, H, pages * page_size
         self.kv_pages = torch.empty((B * pages, page_size, D_QK), dtype=torch.bfloat16, device=dev)
         self.page_table = torch.arange(B * pages, dtype=torch.int32, device=dev).view(B, pages)
         self.lens = torch.zeros(B, dtype=torch.int32, device=dev)
         self.end_pos = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.acc = torch.zeros((B, ld), dtype=torch.float32, device=dev)
-        self.pos = torch.zeros((B, ld), dtype=torch.int32, device=dev)
+        self.acc = torch.zeros((B, self.slots), dtype=torch.float32, device=dev)
+        self.pos = torch.zeros((B, self.slots), dtype=torch.int32, device=dev)
         self.out = torch.empty((B, T, H, D_V), dtype=out_dtype, device=dev)
         self.lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
         with torch.cuda.device(self.lens.device):

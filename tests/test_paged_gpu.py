@@ -768,6 +768,31 @@ def test_cache_object_runs_the_same_calls(cuda_device):
     assert lens.tolist() == [36, 36] and int(one.status.item()) == 0
 
 
+def test_cache_object_appended_to_beyond_its_slots(cuda_device):
+    """40 slots in pages of 16 are 48; a sequence that grows past them is empty
+    for every call, and the other one goes on."""
+    from sparse_attention_04_b200 import api
+    dev, H = cuda_device, 16
+    c = api.PagedLatentCache(2, 40, H=H, page_size=16, out_dtype=torch.float32)
+    assert c.slots == 48
+    c.kv_pages.fill_(NAN)  # what was never written may hold anything
+    c.lens[0] = 30
+    c.kv_pages[:2] = 1.0
+    g = torch.Generator(device=dev).manual_seed(6)
+    for step in range(20):
+        x = torch.randn(2, 1, D, generator=g, device=dev).to(torch.bfloat16)
+        q = torch.randn(2, 1, H, D, generator=g, device=dev).to(torch.bfloat16)
+        out = c.append(x).attend(q, SCALE)
+        acc = c.collect(q, SCALE)
+        torch.cuda.synchronize()
+        full = 31 + step > 48
+        assert int(c.status.item()) == (7 if full else 0), step
+        assert torch.isfinite(out).all() and torch.isfinite(acc).all()
+        assert bool((out[0] == 0).all()) == full and not (out[1] == 0).all()
+    c.evict(24)
+    assert c.lens.tolist() == [50, 20]
+
+
 @pytest.mark.parametrize("H", [128, 16])
 def test_attention_wait_runs_out_then_next_call_is_correct(cuda_device, H):
     """The timeout path (test hook): a bounded wait that never comes true ends the
