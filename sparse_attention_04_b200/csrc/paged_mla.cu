@@ -857,25 +857,27 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   constexpr int kGroups = kCombineWarps / SPLIT;  // column groups per task
   constexpr int kFlight = 8;                       // partials a thread has in flight
   __shared__ CutRow s_cut[kMaxWorkers];
-  __shared__ int s_n;
+  __shared__ int s_count[kCombineWarps];
   __shared__ float s_sum[SPLIT > 1 ? kCombineWarps : 1][10][32];
   grid_dependency_wait();
   allow_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    int n = 0;
-    for (int c0 = 0; c0 < n_workers; c0 += 32) {
-      CutRow c{-1, 0, 0, 0};
-      if (c0 + lane < n_workers) c = cut[c0 + lane];
-      const uint32_t m = __ballot_sync(0xffffffffu, c.q0 >= 0);
-      if (c.q0 >= 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = c;
-      n += __popc(m);
-    }
-    if (lane == 0) s_n = n;
+  // the boundaries that cut a tile, a thread each
+  static_assert(kMaxWorkers <= 32 * kCombineWarps, "a thread per worker");
+  CutRow mine{-1, 0, 0, 0};
+  if (threadIdx.x < n_workers) mine = cut[threadIdx.x];
+  const uint32_t cuts = __ballot_sync(0xffffffffu, mine.q0 >= 0);
+  if (lane == 0) s_count[warp] = __popc(cuts);
+  __syncthreads();
+  int n_cut = 0, at = __popc(cuts & ((1u << lane) - 1u));
+  for (int w = 0; w < kCombineWarps; ++w) {
+    if (w < warp) at += s_count[w];
+    n_cut += s_count[w];
   }
+  if (mine.q0 >= 0) s_cut[at] = mine;
   __syncthreads();
   const int hgroups = (pm + 31) / 32, per_row = hgroups * (kDV / 8 / kGroups);
-  const int tasks = s_n * per_row;
+  const int tasks = n_cut * per_row;
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
     const CutRow c = s_cut[task / per_row];
     const int rest = task % per_row;

@@ -21,7 +21,7 @@
 namespace dsa {
 
 // A tile that part boundaries cut, as the joining kernel sees it.
-struct CutRow {
+struct alignas(16) CutRow {
   int q0;     // first row of out; -1: none
   int first;  // worker of its first partial
   int count;  // partials, one per worker from `first` on
