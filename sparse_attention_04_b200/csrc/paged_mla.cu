@@ -128,7 +128,7 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const PagedMlaParams p) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedMlaParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -250,21 +250,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int valid = 0, valid_next = 0;
         locate(wk.lo, y, valid);
         for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
-          // validity words of the chunk, 16 slots (never more than a box) at a time
-          uint32_t word = ~0u;
-          if (!__all_sync(0xffffffffu, lane >= nbox || valid == p.box)) {
-            word = 0;
-#pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              const int k0 = 32 * (lane & 3) + 16 * hh, bx = k0 / p.box;
-              const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
-              word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
-            }
-          }
-          if (lane < 4) reinterpret_cast<uint32_t*>(smem + kMaskOff)[4 * (g & 3) + lane] = word;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
-          if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
           if (lane < 8) yk[lane] = y;
           __syncwarp();
 #pragma unroll 1
@@ -284,6 +269,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;  // before g counts a chunk that was not sent
           sent = 0;
+          if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
+          // validity words of the chunk, 16 slots (never more than a box) at a time
+          uint32_t word = ~0u;
+          if (!__all_sync(0xffffffffu, lane >= nbox || valid == p.box)) {
+            word = 0;
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              const int k0 = 32 * (lane & 3) + 16 * hh, bx = k0 / p.box;
+              const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
+              word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
+            }
+          }
+          if (lane < 4) reinterpret_cast<uint32_t*>(smem + kMaskOff)[4 * (g & 3) + lane] = word;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
           y = y_next;
           valid = valid_next;
         }

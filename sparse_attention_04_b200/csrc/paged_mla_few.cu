@@ -97,7 +97,7 @@ struct Layout {
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mla_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const PagedMlaParams p) {
+                         const __grid_constant__ PagedMlaParams p) {
   using L = Layout<R>;
   constexpr int C = R / 2;  // rows per consumer warp
   extern __shared__ uint8_t smem_raw[];
@@ -175,21 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       int valid = 0, valid_next = 0;
       if (wk.lo < wk.hi) locate(wk.lo, y, valid);
       for (int i = wk.lo; ok && i < wk.hi; ++i, ++g) {
-        // validity words of the chunk, 16 slots (never more than a box) at a time
-        uint32_t word = ~0u;
-        if (!__all_sync(0xffffffffu, lane >= nbox || valid == p.box)) {
-          word = 0;
-#pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-            const int k0 = 32 * (lane & 1) + 16 * hh, bx = k0 / p.box;
-            const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
-            word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
-          }
-        }
-        if (lane < 2) reinterpret_cast<uint32_t*>(smem + L::kMaskOff)[2 * (g & 3) + lane] = word;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
-        if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
         if (lane < 4) yk[lane] = y;
         __syncwarp();
 #pragma unroll 1
@@ -216,6 +201,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++ropes;
+        if (i + 1 < wk.hi) locate(i + 1, y_next, valid_next);
+        // validity words of the chunk, 16 slots (never more than a box) at a time
+        uint32_t word = ~0u;
+        if (!__all_sync(0xffffffffu, lane >= nbox || valid == p.box)) {
+          word = 0;
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            const int k0 = 32 * (lane & 1) + 16 * hh, bx = k0 / p.box;
+            const int v = __shfl_sync(0xffffffffu, valid, bx) - (k0 - bx * p.box);
+            word |= (v >= 16 ? 0xffffu : v <= 0 ? 0u : (1u << v) - 1u) << (16 * hh);
+          }
+        }
+        if (lane < 2) reinterpret_cast<uint32_t*>(smem + L::kMaskOff)[2 * (g & 3) + lane] = word;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kMaskFull + (g & 3)));
         y = y_next;
         valid = valid_next;
       }
