@@ -840,37 +840,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partials of the cut rows: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// A task is (cut tile, 32 rows, 8 / SPLIT groups of eight columns); lane = row.
+// A task is (cut tile, 32 rows, WARPS / SPLIT groups of eight columns); lane = row.
 // SPLIT warps share a tile's partials, each with the maximum of its own, and
 // the first of them joins their sums in a fixed order: with one long row the
 // partials are many and the rows few (64 partials: 8 loads in flight per
 // thread instead of 64 one behind the other), with many rows it is the other
 // way round.
-constexpr int kCombineWarps = 8;
 constexpr int kMaxWorkers = 256;
 
-template <int SPLIT>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+template <int SPLIT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
                              const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_workers, int pm,
                              void* out, int out_bf16, float* lse) {
-  constexpr int kGroups = kCombineWarps / SPLIT;  // column groups per task
-  constexpr int kFlight = 8;                       // partials a thread has in flight
+  constexpr int kGroups = WARPS / SPLIT;  // column groups per task
+  constexpr int kFlight = 8;              // partials a thread has in flight
   __shared__ CutRow s_cut[kMaxWorkers];
-  __shared__ int s_count[kCombineWarps];
-  __shared__ float s_sum[SPLIT > 1 ? kCombineWarps : 1][10][32];
+  __shared__ int s_count[WARPS];
+  __shared__ float s_sum[SPLIT > 1 ? WARPS : 1][10][32];
   grid_dependency_wait();
   allow_dependents_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the boundaries that cut a tile, a thread each
-  static_assert(kMaxWorkers <= 32 * kCombineWarps, "a thread per worker");
+  static_assert(kMaxWorkers <= 32 * WARPS, "a thread per worker");
   CutRow mine{-1, 0, 0, 0};
   if (threadIdx.x < n_workers) mine = cut[threadIdx.x];
   const uint32_t cuts = __ballot_sync(0xffffffffu, mine.q0 >= 0);
   if (lane == 0) s_count[warp] = __popc(cuts);
   __syncthreads();
   int n_cut = 0, at = __popc(cuts & ((1u << lane) - 1u));
-  for (int w = 0; w < kCombineWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) at += s_count[w];
     n_cut += s_count[w];
   }
@@ -1089,13 +1088,20 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
     // Warps that share a row's partials, by how many a row has at most (one
     // row of 32K: 30.9 us with eight, 33.0 with four, 37.0 with two; two rows
     // 30.9, 28.9, 30.8; eight rows 51.5, 47.5, 43.5 and 42.8 with one, because
-    // the tasks then fill the card several times over).
-    const int per_row = n / p.n_rows, split = per_row >= 64 ? 8 : per_row >= 16 ? 4 : 1;
-    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8) * split / kCombineWarps;
-    const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * kCombineWarps);
-    const auto kernel = split == 8   ? paged_mla_combine_kernel<8>
-                        : split == 4 ? paged_mla_combine_kernel<4>
-                                     : paged_mla_combine_kernel<1>;
+    // the tasks then fill the card several times over).  A tile of few rows has
+    // few tasks, more warps fit beside one another (16 heads, back to back: one
+    // row of 32K 18.6 us with eight, 17.4 with sixteen, four rows 25.0 with four,
+    // 23.8 with eight; 128 heads the other way round, 24.6 and 26.7).
+    const int per_row = n / p.n_rows;
+    const bool few = few_rows(T, H);
+    const int split = per_row >= 64 ? (few ? 16 : 8) : few && per_row >= 32 ? 8 : per_row >= 16 ? 4 : 1;
+    const int warps = std::max(split, 8), groups = warps / split;  // column groups per task
+    const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8 / groups);
+    const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * warps);
+    const auto kernel = split == 16  ? paged_mla_combine_kernel<16, 16>
+                        : split == 8 ? paged_mla_combine_kernel<8, 8>
+                        : split == 4 ? paged_mla_combine_kernel<4, 8>
+                                     : paged_mla_combine_kernel<1, 8>;
     if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float*)p.part_sc, (const uint4*)p.part_o,
                    n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;
