@@ -45,7 +45,7 @@
 // the way of a message (it flushes the thread's earlier stores first, 2000
 // cycles) 0.70 -> 0.61.  Measured slower: requesting later chunks into L2 ahead
 // (0.55 -> 0.63 ms and more), P through the copy engine (behind the block loads
-// in its queue).  One 2K row takes 20.6 us and one 32K row 28.8, most of it
+// in its queue).  One 2K row takes 17.2 us and one 32K row 24.6, most of it
 // latency: query into TMEM, one chunk through both CTAs, the partial's stores,
 // the joining kernel.
 #include <cuda.h>
