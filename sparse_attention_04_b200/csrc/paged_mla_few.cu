@@ -21,12 +21,13 @@
 // rescaled only when it rose by more than 2^8.  A row's sum stays per lane
 // until the part ends.
 //
-// What bounds it (B200).  24 sequences of up to 30K slots (423 MB), two tokens of 16 heads: 94 us, 65 of
-// them the bytes at the measured copy rate (the CTA pair of paged_mla.cu: 117;
-// a ring of eight pieces: 98).  A chunk takes about 3400 cycles, 1350 of them
-// in the consumers; without loads the whole call takes 76.  The rest is latency
-// at both ends: one row of 2K takes 12.7 us, one of 32K 17.4 (16 heads, ten calls
-// in a graph).
+// What bounds it (B200).  24 sequences of up to 30K slots (423 MB), two tokens
+// of 16 heads: 94 us, 65 of them the bytes at the measured copy rate (the CTA
+// pair of paged_mla.cu: 117; a ring of eight pieces: 98); 32 sequences of 8K to
+// 128K slots, 16 heads: 465 of 451.  A chunk takes about 3400 cycles, 1350 of
+// them in the consumers; without loads the first case takes 76.  The rest is
+// latency at both ends: one row of 2K takes 12.7 us, one of 32K 17.4 (16 heads,
+// ten calls in a graph).
 #include "paged_mla.cuh"
 #include "tmap.h"
 
