@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t named_barrier_count(uint32_t id, uint32_t nt
 // Maximum over the warp's lanes; NaN counts as absent unless all are NaN.
 __device__ __forceinline__ float warp_max(float x) {
   float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 
