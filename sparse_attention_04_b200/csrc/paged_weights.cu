@@ -19,7 +19,8 @@
 // list of all sequences' 128-slot chunks.
 //
 // B200: 16 sequences of 1K to 65K slots, 128 heads (560 K slots, 644 MB): 106 us
-// in a row, 119 with changing inputs, 6.1 and 5.4 TB/s; one 32K sequence 12 us.
+// in a row, 119 with changing inputs, 6.1 and 5.4 TB/s; one 32K sequence 9.5 us in
+// a row, 13 with changing inputs.
 //
 // Roles: warps 0-7 epilogue, warp 8 loader, warp 9 TMEM allocator and MMA
 // issuer.  S has two TMEM buffers, so that the exponentials of a chunk run
@@ -54,7 +55,7 @@ struct Misc {
   alignas(16) int32_t y[8];  // row coordinates of a chunk's boxes
   float part[2][4][kChunk];  // sums over 32 rows each, by chunk parity
   int tmem_base, abort, first_seq, pad;
-  int64_t first_unit, total_units, share;
+  int64_t first_unit;
   int64_t warp_sum[kThreads / 32];
 };
 constexpr int kQ8Off = (int)((sizeof(Misc) + 1023) / 1024 * 1024);
@@ -107,7 +108,7 @@ struct Walk {
 
 __global__ void __launch_bounds__(kThreads, 1)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const PagedWeightsParams p) {
+                         const __grid_constant__ PagedWeightsParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -130,8 +131,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();  // everything may come from the previous kernel
   allow_dependents_launch();
-  {
-    // units (chunks) of all sequences, and the one this CTA's part begins in
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
+  // ---- units (chunks) of all sequences, and the one this CTA's part begins in
+  Walk wk;
+  wk.n_seq = p.B;
+  int64_t total;
+  constexpr int kPer = 4;
+  if (p.B <= 32 * kPer) {
+    // every warp for itself, a lane takes up to four sequences (one 32K
+    // sequence: 9.5 us, with the CTA's threads 9.95)
+    const int per = (p.B + 31) >> 5;
+    int64_t units[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = lane * per + i;
+      bool bad = false;
+      units[i] = i < per && b < p.B ? n_chunks_of(seq_len(p, b, bad)) : 0;
+      if (bad && blockIdx.x == 0 && warp == 0) report(p.status, DSA_ERR_BAD_OFFSETS);
+      mine += units[i];
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    wk.w0 = ceil_div(total, (int)gridDim.x) * blockIdx.x;
+    wk.b = p.B;
+    wk.u = 0;
+    const uint32_t has = __ballot_sync(0xffffffffu, inc - mine <= wk.w0 && wk.w0 < inc);
+    if (has) {
+      int b = lane * per;
+      int64_t u = inc - mine, next = u;
+#pragma unroll
+      for (int i = 0; i < kPer - 1; ++i) {
+        next += units[i];
+        if (i + 1 < per && wk.w0 >= next) {
+          u = next;
+          b = lane * per + i + 1;
+        }
+      }
+      const int src = __ffs((int)has) - 1;
+      wk.b = __shfl_sync(0xffffffffu, b, src);
+      wk.u = __shfl_sync(0xffffffffu, u, src);
+    }
+  } else {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
     int64_t mine = 0;
@@ -149,19 +197,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) misc->warp_sum[warp] = inc;
     __syncthreads();
     // every warp adds the warps' sums up for itself
-    int64_t total = lane < kThreads / 32 ? misc->warp_sum[lane] : 0, before = lane < warp ? total : 0;
+    total = lane < kThreads / 32 ? misc->warp_sum[lane] : 0;
+    int64_t before = lane < warp ? total : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       total += __shfl_xor_sync(0xffffffffu, total, o);
       before += __shfl_xor_sync(0xffffffffu, before, o);
     }
     before += inc - mine;
-    const int64_t share = ceil_div(total, (int)gridDim.x), w0 = share * blockIdx.x;
-    if (threadIdx.x == 0) {
-      misc->total_units = total;
-      misc->share = share;
-      if (w0 >= total) misc->first_seq = p.B;
-    }
+    const int64_t w0 = ceil_div(total, (int)gridDim.x) * blockIdx.x;
+    if (threadIdx.x == 0 && w0 >= total) misc->first_seq = p.B;
     if (before <= w0 && w0 < before + mine) {
       int64_t u = before;
       for (int b = b0; b < b1; ++b) {
@@ -175,18 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         u += c;
       }
     }
+    __syncthreads();
+    wk.w0 = ceil_div(total, (int)gridDim.x) * blockIdx.x;
+    wk.b = misc->first_seq;
+    wk.u = wk.b < p.B ? misc->first_unit : 0;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc->tmem_base);
-  Walk wk;
-  const int64_t share = misc->share;
-  wk.w0 = share * blockIdx.x;
-  wk.w1 = min(wk.w0 + share, misc->total_units);
-  wk.b = misc->first_seq;
-  wk.n_seq = p.B;
-  wk.u = wk.b < p.B ? misc->first_unit : 0;
+  wk.w1 = min(wk.w0 + ceil_div(total, (int)gridDim.x), total);
   const int th = p.T * p.H, n_tiles = (th + kRows - 1) / kRows;
 
   if (warp == kLoadWarp) {

@@ -430,6 +430,24 @@ def test_weights_on_a_bad_page_only_decay(cuda_device):
     assert torch.equal(out[1, :130], good[1, :130])
 
 
+@pytest.mark.parametrize("B", [31, 128, 129, 330])
+def test_weights_of_many_sequences(cuda_device, B):
+    """Few and many sequences find their parts in two ways; a bad length among
+    them is reported and empty."""
+    g = torch.Generator().manual_seed(B)
+    lens = (torch.randint(0, 500, (B,), generator=g) * (torch.rand(B, generator=g) < 0.8)).tolist()
+    c = Cache(cuda_device, lens, 32, seed=B)
+    q = _q(c, B, 1, 8)
+    out, lse, st = _attend(c, q)
+    assert st == 0
+    acc = torch.rand(B, 512, generator=c.g, device=c.dev)
+    _, st = _check_weights(c, q, lse, acc, 0.5)
+    assert st == 0
+    c.lens[B // 2], c.lens_py[B // 2] = -4, 0
+    _, st = _check_weights(c, q, lse, acc, 0.5)
+    assert st == 7
+
+
 def test_weights_of_an_empty_row_add_nothing(cuda_device):
     """lse = -inf: the row saw nothing."""
     c = Cache(cuda_device, [64], 64, seed=14)
