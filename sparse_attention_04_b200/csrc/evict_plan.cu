@@ -7,6 +7,8 @@
 // and how many keys equal to tau stay (the lowest slots), and two prefix
 // counts over the resulting bitmap rank the free slots below n and the
 // survivors from n on: the i-th of one takes the i-th of the other.
+// (Where the protected slots alone are more than n, the n-th key is all ones and
+// a second search ranks them by their weight.)
 //
 // One thread-block cluster per sequence; CTA r owns the contiguous slots
 // [r * S, (r + 1) * S).  The slots' acc and pos are read from memory once
@@ -60,9 +62,12 @@ struct PlanArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ uint32_t slot_key(float a, bool kept_always) {
-  if (kept_always) return 0xffffffffu;
-  return a != a ? 0u : float_order_key(a);  // -inf maps above 0
+// among: only the protected slots compete (0 for the others; -inf maps far
+// above 1).
+__device__ __forceinline__ uint32_t slot_key(float a, bool kept_always, bool among) {
+  const uint32_t key = a != a ? 0u : float_order_key(a);
+  if (among) return kept_always ? max(key, 1u) : 0u;
+  return kept_always ? 0xffffffffu : key;
 }
 
 // Exclusive scan over the block of one value per thread; *total is the sum.
@@ -132,10 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
   const int s_lo = min(rank * S, L), m = min(s_lo + S, L) - s_lo;  // this CTA's slots
   const float* const acc = a.acc + (int64_t)b * a.ld + s_lo;
   const int32_t* const pos = a.recent > 0 ? a.pos + (int64_t)b * a.ld + s_lo : nullptr;
-  auto make_key = [&](int i) { return slot_key(acc[i], pos && pos[i] >= protect_from); };
+  // More protected slots than the budget holds (positions that repeat, an
+  // end_pos that lags): they compete among themselves, in a second search.
+  bool among = false;
+  auto make_key = [&](int i) { return slot_key(acc[i], pos && pos[i] >= protect_from, among); };
 
-  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
-  __syncthreads();
   // Adds four keys per lane to a histogram.  A warp whose keys are all alike
   // (fresh slots, say) adds once; otherwise the few lanes that share a bin are
   // served one after the other, which costs less than sorting them out.
@@ -150,42 +156,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     for (int e = 0; e < 4; ++e)
       if (on[e]) atomicAdd(&hist[bin[e]], 1u);
   };
-  // ---- keys, four slots per thread at a time and kFlight such groups in
-  // flight, and the histogram of their top 11 bits
-  constexpr int kFlight = 2;
-  const int m4 = (m + 3) / 4;
-  for (int g0 = 0; g0 < m4; g0 += kFlight * kThreads) {
-    float4 av[kFlight];
-    int4 pv[kFlight];
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const int g = g0 + k * kThreads + threadIdx.x;
-      av[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      pv[k] = make_int4(INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN);
-      if (4 * g < m) {  // (whole groups: the rows' pitch is a multiple of 4)
-        av[k] = __ldcs(reinterpret_cast<const float4*>(acc) + g);
-        if (pos) pv[k] = __ldcs(reinterpret_cast<const int4*>(pos) + g);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const int g = g0 + k * kThreads + threadIdx.x;
-      if (__all_sync(0xffffffffu, 4 * g >= m)) break;
-      const float a4[4] = {av[k].x, av[k].y, av[k].z, av[k].w};
-      const int p4[4] = {pv[k].x, pv[k].y, pv[k].z, pv[k].w};
-      uint32_t key[4], bin[4];
-      bool on[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        key[e] = slot_key(a4[e], pos && p4[e] >= protect_from);
-        bin[e] = key[e] >> 21;
-        on[e] = 4 * g + e < m;
-      }
-      count4(sm.hist[0], bin, on);
-      if (4 * g < key_cap) *reinterpret_cast<uint4*>(keys + 4 * g) = make_uint4(key[0], key[1], key[2], key[3]);
-    }
-  }
-  __syncthreads();
   // keys of the slots 4g .. 4g + 3 (those at or behind m are of no meaning)
   auto keys_of = [&](int g) -> uint4 {
     if (4 * g < key_cap) return *reinterpret_cast<const uint4*>(keys + 4 * g);
@@ -197,72 +167,118 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanArgs 
     return k;
   };
   auto key_of = [&](int i) { return i < key_cap ? keys[i] : make_key(i); };
-  // ---- three digit passes: tau, and how many keys equal to it stay
-  uint32_t prefix = 0, remaining = (uint32_t)n;
+  // ---- keys, four slots per thread at a time and kFlight such groups in
+  // flight, and the histogram of their top 11 bits
+  constexpr int kFlight = 2;
+  const int m4 = (m + 3) / 4;
+  uint32_t prefix, remaining;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bins = pass == 2 ? 1024 : 2048;
-    if (pass > 0) {
-      const int pshift = pass == 1 ? 21 : 10;
-      for (int g0 = 0; g0 < m4; g0 += kThreads) {
-        const int g = g0 + threadIdx.x;
-        const uint4 k4 = g < m4 ? keys_of(g) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+  for (;;) {
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+    __syncthreads();
+    for (int g0 = 0; g0 < m4; g0 += kFlight * kThreads) {
+      float4 av[kFlight];
+      int4 pv[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const int g = g0 + k * kThreads + threadIdx.x;
+        av[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        pv[k] = make_int4(INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN);
+        if (4 * g < m) {  // (whole groups: the rows' pitch is a multiple of 4)
+          av[k] = __ldcs(reinterpret_cast<const float4*>(acc) + g);
+          if (pos) pv[k] = __ldcs(reinterpret_cast<const int4*>(pos) + g);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const int g = g0 + k * kThreads + threadIdx.x;
+        if (__all_sync(0xffffffffu, 4 * g >= m)) break;
+        const float a4[4] = {av[k].x, av[k].y, av[k].z, av[k].w};
+        const int p4[4] = {pv[k].x, pv[k].y, pv[k].z, pv[k].w};
+        uint32_t key[4], bin[4];
         bool on[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) on[e] = 4 * g + e < m && (key[e] >> pshift) == (prefix >> pshift);
-        if (!__any_sync(0xffffffffu, on[0] || on[1] || on[2] || on[3])) continue;  // mostly: few keys share a prefix
-        uint32_t bin[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bin[e] = (key[e] >> shift) & (uint32_t)(bins - 1);
-        count4(sm.hist[pass], bin, on);
+        for (int e = 0; e < 4; ++e) {
+          key[e] = slot_key(a4[e], pos && p4[e] >= protect_from, among);
+          bin[e] = key[e] >> 21;
+          on[e] = 4 * g + e < m;
+        }
+        count4(sm.hist[0], bin, on);
+        if (4 * g < key_cap) *reinterpret_cast<uint4*>(keys + 4 * g) = make_uint4(key[0], key[1], key[2], key[3]);
       }
     }
-    meet();
-    // The bin, from the top, that holds the remaining-th largest key: lane l of
-    // warp w has the bins bins-1 - 64 w - 2 l and the one below, summed over the
-    // cluster.  The warps' sums say which warp has it, and that one looks
-    // inside.
-    const int hi = bins - 1 - 64 * warp - 2 * lane;
-    uint32_t c0 = 0, c1 = 0;
-    if (hi > 0) {
-      for (int q = 0; q < CS; ++q) {
-        const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[pass][0], q) + hi - 1);
-        c0 += v.y;
-        c1 += v.x;
-      }
-    }
-    const uint32_t mine = __reduce_add_sync(0xffffffffu, c0 + c1);
-    if (lane == 0) sm.warp_sum[pass][warp] = mine;
     __syncthreads();
-    const uint32_t t = sm.warp_sum[pass][lane];
-    uint32_t inc = t;
+    // ---- three digit passes: tau, and how many keys equal to it stay
+    prefix = 0;
+    remaining = (uint32_t)n;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const int bins = pass == 2 ? 1024 : 2048;
+      if (pass > 0) {
+        const int pshift = pass == 1 ? 21 : 10;
+        for (int g0 = 0; g0 < m4; g0 += kThreads) {
+          const int g = g0 + threadIdx.x;
+          const uint4 k4 = g < m4 ? keys_of(g) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+          bool on[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    uint32_t above = __shfl_sync(0xffffffffu, inc - t, warp);
-    if (above < remaining && remaining <= above + mine) {
-      inc = c0 + c1;
+          for (int e = 0; e < 4; ++e) on[e] = 4 * g + e < m && (key[e] >> pshift) == (prefix >> pshift);
+          if (!__any_sync(0xffffffffu, on[0] || on[1] || on[2] || on[3])) continue;  // mostly: few keys share a prefix
+          uint32_t bin[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bin[e] = (key[e] >> shift) & (uint32_t)(bins - 1);
+          count4(sm.hist[pass], bin, on);
+        }
+      }
+      meet();
+      // The bin, from the top, that holds the remaining-th largest key: lane l of
+      // warp w has the bins bins-1 - 64 w - 2 l and the one below, summed over the
+      // cluster.  The warps' sums say which warp has it, and that one looks
+      // inside.
+      const int hi = bins - 1 - 64 * warp - 2 * lane;
+      uint32_t c0 = 0, c1 = 0;
+      if (hi > 0) {
+        for (int q = 0; q < CS; ++q) {
+          const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[pass][0], q) + hi - 1);
+          c0 += v.y;
+          c1 += v.x;
+        }
+      }
+      const uint32_t mine = __reduce_add_sync(0xffffffffu, c0 + c1);
+      if (lane == 0) sm.warp_sum[pass][warp] = mine;
+      __syncthreads();
+      const uint32_t t = sm.warp_sum[pass][lane];
+      uint32_t inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += u;
       }
-      above += inc - (c0 + c1);
-      if (above < remaining && remaining <= above + c0 + c1) {
-        const bool second = remaining > above + c0;
-        sm.digit = (uint32_t)(second ? hi - 1 : hi);
-        sm.remaining = remaining - above - (second ? c0 : 0u);
-        sm.bin_count = second ? c1 : c0;
+      uint32_t above = __shfl_sync(0xffffffffu, inc - t, warp);
+      if (above < remaining && remaining <= above + mine) {
+        inc = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += u;
+        }
+        above += inc - (c0 + c1);
+        if (above < remaining && remaining <= above + c0 + c1) {
+          const bool second = remaining > above + c0;
+          sm.digit = (uint32_t)(second ? hi - 1 : hi);
+          sm.remaining = remaining - above - (second ? c0 : 0u);
+          sm.bin_count = second ? c1 : c0;
+        }
       }
+      __syncthreads();
+      prefix |= sm.digit << shift;
+      remaining = sm.remaining;
+      if (pass < 2) __syncthreads();  // read before the next pass writes them
     }
-    __syncthreads();
-    prefix |= sm.digit << shift;
-    remaining = sm.remaining;
-    if (pass < 2) __syncthreads();  // read before the next pass writes them
+    if (among || prefix != 0xffffffffu || sm.bin_count == remaining) break;  // (the same in every CTA)
+    among = true;
+    meet();  // the histograms are read
   }
   const uint32_t tau = prefix, need_eq = remaining;
   if (warp == 0) {  // keys equal to tau in the CTAs before this one

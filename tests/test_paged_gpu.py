@@ -569,6 +569,21 @@ def test_plan_of_ties_and_special_values(cuda_device, ld):
     _check_plan(acc, None, [ld] * 5, None, ld // 2, 0)
 
 
+@pytest.mark.parametrize("ld", [8, 1000, 20000, 400000])
+def test_plan_with_more_protected_slots_than_the_budget(cuda_device, ld):
+    """Positions that repeat, or an end_pos that lags: the protected slots
+    compete by weight, NaN last, then by slot; the others stay out."""
+    g = torch.Generator(device=cuda_device).manual_seed(ld)
+    vals = torch.tensor([0.0, -0.0, 2.5, -1.0, float("inf"), float("-inf"), NAN, 3e38], device=cuda_device)
+    acc = torch.randn(4, ld, generator=g, device=cuda_device).exp_()
+    acc[1] = vals[torch.randint(0, 8, (ld,), generator=g, device=cuda_device)]
+    acc[2] = NAN
+    pos = torch.randint(0, 10, (4, ld), generator=g, device=cuda_device, dtype=torch.int32)
+    pos[3] = 9  # every slot
+    for budget, recent in ((max(2, ld // 8), 2), (ld // 2, min(6, ld // 2)), (1, 1)):
+        _check_plan(acc, pos, [ld, ld, ld, ld - 1], [10] * 4, budget, recent)
+
+
 def test_plan_of_a_sequence_beyond_shared_memory(cuda_device):
     ld = 500000  # more keys than eight CTAs hold on chip
     g = torch.Generator(device=cuda_device).manual_seed(1)
