@@ -185,7 +185,9 @@ class PagedLatentCache:
     pages out writes its own numbers into page_table.  Set lens (and end_pos,
     the tokens seen so far) after filling the first rows, or append the prompt
     in calls of T tokens.  A sequence appended to beyond its slots is reported in
-    status and counts as empty until lens is set again.
+    status and counts as empty until lens is set again.  max_moves: rows an
+    eviction may move per sequence, enough for every cut unless given; a sequence
+    that needs more is reported in status and not cut.
 
     kv_pages [pages, page_size, 576] bf16, page_table [B, pages per sequence],
     lens and end_pos [B], acc and pos [B, slots] (see include/dsa.h)."""
@@ -206,7 +208,8 @@ class PagedLatentCache:
         with torch.cuda.device(self.lens.device):
             nbytes = _lib.paged_mla_workspace_size(B, T, H)
         self.workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-        moves = max(1, max_moves if max_moves is not None else slots // 2)
+        # a cut of L slots to n moves min(n, L - n) rows at most
+        moves = max(1, max_moves if max_moves is not None else self.slots // 2)
         self.new_lens, self.n_moves = torch.zeros_like(self.lens), torch.zeros_like(self.lens)
         self.move_dst = torch.empty((B, moves), dtype=torch.int32, device=dev)
         self.move_src = torch.empty((B, moves), dtype=torch.int32, device=dev)
