@@ -182,9 +182,8 @@ class PagedLatentCache:
     Lengths, positions and the eviction plan stay on the device, so that the
     whole step can be captured in one CUDA graph.  Every sequence has page
     lists for `slots` slots, rounded up to whole pages; a scheduler that hands
-    pages out writes its own numbers into page_table.  Set lens (and end_pos,
-    the tokens seen so far) after filling the first rows, or append the prompt
-    in calls of T tokens.  A sequence appended to beyond its slots is reported in
+    pages out writes its own numbers into page_table.  Append the prompt, or
+    write its rows into kv_pages and call fill.  A sequence appended to beyond its slots is reported in
     status and counts as empty until lens is set again.  max_moves: rows an
     eviction may move per sequence, enough for every cut unless given; a sequence
     that needs more is reported in status and not cut.
@@ -214,6 +213,16 @@ class PagedLatentCache:
         self.move_dst = torch.empty((B, moves), dtype=torch.int32, device=dev)
         self.move_src = torch.empty((B, moves), dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def fill(self, lens):
+        """The first lens[b] slots of every sequence hold its tokens 0 .. lens[b] - 1
+        (rows written into kv_pages directly): sets lens, end_pos, pos and acc,
+        whatever they held before."""
+        self.lens.copy_(torch.as_tensor(lens))
+        self.end_pos.copy_(self.lens)
+        self.pos.copy_(torch.arange(self.slots, dtype=torch.int32, device=self.pos.device).expand_as(self.pos))
+        self.acc.zero_()
+        return self
 
     def append(self, kv_new):
         """The T newest tokens' rows [B,T,576] of every sequence."""

@@ -42,3 +42,22 @@ def test_a_given_limit_of_moves_is_kept_and_reported(cuda_device):
     c.status.zero_()
     c.evict(61)
     assert int(c.status.item()) == 0 and int(c.lens.item()) == 61
+
+
+def test_filled_rows_have_positions(cuda_device):
+    """After fill, an eviction knows which tokens are the newest; appended tokens
+    go on behind them, and a second fill starts afresh."""
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    c = _cache(2, 64, H=16, page_size=16)
+    for lens in ([50, 7], torch.tensor([64, 1], device=cuda_device)):
+        c.kv_pages.copy_(torch.randn(c.kv_pages.shape, generator=g, device=cuda_device))
+        c.fill(lens)
+        n = torch.as_tensor(lens).tolist()
+        assert c.lens.tolist() == n and c.end_pos.tolist() == n and not c.acc.any()
+        c.acc[0, :30] = 1.0  # the newest tokens weigh nothing
+        c.evict(20, 8)
+        assert c.lens.tolist() == [min(20, k) for k in n] and int(c.status.item()) == 0
+        assert set(range(n[0] - 8, n[0])) <= set(c.pos[0, :20].tolist())
+        assert c.pos[1, :n[1]].tolist() == list(range(n[1]))
+        c.append(_rows(g, 2, 1))
+        assert c.pos[0, 20].item() == n[0] and c.pos[1, n[1]].item() == n[1]
