@@ -224,12 +224,20 @@ class PagedLatentCache:
         self.acc.zero_()
         return self
 
-    def append(self, kv_new):
-        """The T newest tokens' rows [B,T,576] of every sequence."""
-        self.lens.add_(kv_new.shape[1])
-        self.end_pos.add_(kv_new.shape[1])
-        _lib.paged_append(kv_new, self.kv_pages, self.page_table, self.lens, acc=self.acc, pos=self.pos,
-                          end_pos=self.end_pos, status=self.status)
+    def append(self, kv_new, active=None):
+        """The newest tokens' rows [B,T,576], any T, of every sequence, or of those
+        where active [B] (bool) holds: the others keep what they have, and an
+        empty one stays empty.  Prompts of different lengths go in one by one."""
+        T, lens = kv_new.shape[1], self.lens
+        if active is None:
+            self.lens.add_(T)
+            self.end_pos.add_(T)
+        else:
+            self.lens.add_(active, alpha=T)
+            self.end_pos.add_(active, alpha=T)
+            lens = self.lens * active  # an empty sequence is not written
+        _lib.paged_append(kv_new, self.kv_pages, self.page_table, lens, acc=self.acc, pos=self.pos, end_pos=self.end_pos,
+                          status=self.status)
         return self
 
     def attend(self, q, scale):

@@ -61,3 +61,43 @@ def test_filled_rows_have_positions(cuda_device):
         assert c.pos[1, :n[1]].tolist() == list(range(n[1]))
         c.append(_rows(g, 2, 1))
         assert c.pos[0, 20].item() == n[0] and c.pos[1, n[1]].item() == n[1]
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_sequences_that_rest_keep_what_they_have(cuda_device, graph):
+    """A padded batch: an empty sequence stays empty, a finished one is not
+    written, the others grow."""
+    g = torch.Generator(device=cuda_device).manual_seed(2)
+    c = _cache(4, 64, H=16, page_size=16, out_dtype=torch.float32)
+    c.kv_pages.fill_(float("nan"))
+    for b, n in ((1, 5), (3, 17)):  # prompts of different lengths, one by one
+        c.append(_rows(g, 4, n), active=torch.arange(4, device=cuda_device) == b)
+    assert c.lens.tolist() == [0, 5, 0, 17]
+    active = torch.tensor([False, True, True, False], device=cuda_device)
+    x = _rows(g, 4, 1)
+    run = lambda: c.append(x, active=active)
+    if graph:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        cg = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(cg, stream=s):
+            run()
+        run = cg.replay
+    for step in range(20):
+        before, pos, acc = c.kv_pages.clone(), c.pos.clone(), c.acc.clone()
+        x.copy_(_rows(g, 4, 1))
+        c.acc.add_(1)
+        run()
+        torch.cuda.synchronize()
+        assert c.lens.tolist() == [0, 6 + step, 1 + step, 17] and c.end_pos.tolist() == c.lens.tolist()
+        acc += 1
+        for b in (1, 2):
+            s = int(c.lens[b]) - 1
+            before.view(4, 64, D)[b, s], pos[b, s], acc[b, s] = x[b, 0], s, 0
+        assert torch.equal(c.kv_pages.view(torch.int16), before.view(torch.int16))
+        assert torch.equal(c.pos, pos) and torch.equal(c.acc, acc)
+    out = c.attend(_rows(g, 4, 1, 16), SCALE)
+    torch.cuda.synchronize()
+    assert torch.all(out[0] == 0) and torch.all(c.lse[0] == float("-inf"))
+    assert torch.isfinite(out).all() and int(c.status.item()) == 0
