@@ -180,13 +180,15 @@ class PagedLatentCache:
         cache.evict(budget, recent)                    # keep the heaviest and newest
 
     Lengths, positions and the eviction plan stay on the device, so that the
-    whole step can be captured in one CUDA graph.  Every sequence has page
-    lists for `slots` slots, rounded up to whole pages; a scheduler that hands
-    pages out writes its own numbers into page_table.  Append the prompt, or
-    write its rows into kv_pages and call fill.  A sequence appended to beyond its slots is reported in
-    status and counts as empty until lens is set again.  max_moves: rows an
-    eviction may move per sequence, enough for every cut unless given; a sequence
-    that needs more is reported in status and not cut.
+    whole step can be captured in one CUDA graph.  T: most tokens of a sequence
+    that attend to the cache in one call (a prompt's, say; single tokens go
+    through the same object).  Every sequence has page lists for `slots` slots,
+    rounded up to whole pages; a scheduler that hands pages out writes its own
+    numbers into page_table.  Append the prompt, or write its rows into kv_pages
+    and call fill.  A sequence appended to beyond its slots is reported in status
+    and counts as empty until lens is set again.  max_moves: rows an eviction may
+    move per sequence, enough for every cut unless given; a sequence that needs
+    more is reported in status and not cut.
 
     kv_pages [pages, page_size, 576] bf16, page_table [B, pages per sequence],
     lens and end_pos [B], acc and pos [B, slots] (see include/dsa.h)."""
@@ -204,8 +206,8 @@ class PagedLatentCache:
         self.pos = torch.zeros((B, self.slots), dtype=torch.int32, device=dev)
         self.out = torch.empty((B, T, H, D_V), dtype=out_dtype, device=dev)
         self.lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
-        with torch.cuda.device(self.lens.device):
-            nbytes = _lib.paged_mla_workspace_size(B, T, H)
+        with torch.cuda.device(self.lens.device):  # fewer tokens may need more: their tiles go to another kernel
+            nbytes = max(_lib.paged_mla_workspace_size(B, t, H) for t in range(1, max(1, min(T, 128 // max(H, 1))) + 1))
         self.workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
         # a cut of L slots to n moves min(n, L - n) rows at most
         moves = max(1, max_moves if max_moves is not None else self.slots // 2)
@@ -240,15 +242,26 @@ class PagedLatentCache:
                           status=self.status)
         return self
 
+    def _rows(self, q):
+        """out and lse of a call with q's number of tokens: the first elements of self.out and self.lse."""
+        t = q.shape[1] if q.dim() == 4 else 0
+        if t == self.T:
+            return self.out, self.lse
+        if not 0 < t < self.T:
+            raise _lib.DSAError(1, f"PagedLatentCache: q must be [B, T, H, 576] with 1 to {self.T} tokens")
+        n = self.B * t * self.H
+        return (self.out.view(-1, D_V)[:n].view(self.B, t, self.H, D_V), self.lse.view(-1)[:n].view(self.B, t, self.H))
+
     def attend(self, q, scale):
-        """Attention of q [B,T,H,576] over each whole cache: out [B,T,H,512]; lse beside it."""
-        _lib.paged_mla(q, self.kv_pages, self.page_table, self.lens, scale, self.out, lse=self.lse,
-                       workspace=self.workspace, status=self.status)
-        return self.out
+        """Attention of q [B,t,H,576], t <= T, over each whole cache: out [B,t,H,512]; lse beside it."""
+        out, lse = self._rows(q)
+        _lib.paged_mla(q, self.kv_pages, self.page_table, self.lens, scale, out, lse=lse, workspace=self.workspace,
+                       status=self.status)
+        return out
 
     def collect(self, q, scale, decay=1.0):
         """Adds the weight that the slots got from the last attend's q to acc."""
-        _lib.paged_weights(q, self.kv_pages, self.page_table, self.lens, self.lse, scale, self.acc, decay=decay,
+        _lib.paged_weights(q, self.kv_pages, self.page_table, self.lens, self._rows(q)[1], scale, self.acc, decay=decay,
                            status=self.status)
         return self.acc
 

@@ -101,3 +101,29 @@ def test_sequences_that_rest_keep_what_they_have(cuda_device, graph):
     torch.cuda.synchronize()
     assert torch.all(out[0] == 0) and torch.all(c.lse[0] == float("-inf"))
     assert torch.isfinite(out).all() and int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("T,H", [(4, 16), (7, 16), (3, 16), (2, 128), (40, 3), (5, 33)])
+def test_prompt_chunks_and_single_tokens_through_one_object(cuda_device, T, H):
+    """Calls with fewer tokens than the object was made for give the bits of an
+    object made for that many."""
+    g = torch.Generator(device=cuda_device).manual_seed(T + H)
+    c = _cache(3, 3000, T=T, H=H, page_size=32)
+    c.append(_rows(g, 3, 2900), active=torch.tensor([True, False, True], device=cuda_device))
+    c.append(_rows(g, 3, T))
+    for t in sorted({T, 1, 2, T - 1} - {0}, reverse=True):
+        q = _rows(g, 3, t, H)
+        one = _cache(3, 3000, T=t, H=H, page_size=32)
+        for name in ("kv_pages", "lens", "end_pos", "acc", "pos"):
+            getattr(one, name).copy_(getattr(c, name))
+        assert one.workspace.numel() <= c.workspace.numel()
+        out, want = c.attend(q, SCALE), one.attend(q, SCALE)
+        assert out.shape == want.shape and torch.equal(out, want)
+        assert torch.equal(c.collect(q, SCALE, 0.5), one.collect(q, SCALE, 0.5))
+    assert int(c.status.item()) == 0
+    from sparse_attention_04_b200 import _lib
+    for bad in (_rows(g, 3, T + 1, H), _rows(g, 3, 0, H), _rows(g, 2, T, H), _rows(g, 3, T)):
+        with pytest.raises(_lib.DSAError):
+            c.attend(bad, SCALE)
+        with pytest.raises(_lib.DSAError):
+            c.collect(bad, SCALE)
