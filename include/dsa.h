@@ -303,6 +303,11 @@ int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* pag
  * is divided by the lengths found on the device, so ragged batches need no
  * padding and no plan.  The result does not depend on what else runs; the same
  * inputs give the same bits.
+ * Roundings: p is rounded to bf16 before its product with kv (half a step,
+ * 2^-8), whatever the output's type; the sum of p that divides it is not.  All
+ * sums are fp32, with one exception: with bf16 output and tiles of more than 32
+ * rows, the partial sums of a row that several SMs share are stored as scaled
+ * fp16 (2^-11) before they are added up.
  * workspace: dsa_paged_mla_workspace_size(B, T, H) bytes, for the current
  * device; its contents need not survive between calls, and calls that may run
  * at the same time (two graphs, two streams) need one each.

@@ -709,16 +709,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool whole = wk.hi - wk.lo == wk.chunks;
         const float mul = l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
         const int64_t part = 2 * cl + (wk.lo > 0 ? 0 : 1);
-        // Partials: fp16, each row's 32 columns scaled by the power of two that
-        // brings the largest of them to [1, 2): 11 bits, against the 8 that P
-        // has and a bf16 output keeps, and half the bytes of fp32.  (An SM
-        // writes 28 bytes a cycle, however it writes: a 128-row fp32 partial
-        // takes 9000 cycles.)  [column / 8][row][8], so that a warp's stores
+        // Partials: fp32 where the output is.  With bf16 output fp16, each
+        // row's 32 columns scaled by the power of two that brings the largest of
+        // them to [1, 2): 11 bits, against the 8 that P has and the output
+        // keeps, and half the bytes (an SM writes 28 bytes a cycle, however it
+        // writes: a 128-row fp32 partial takes 9000 cycles).  With nothing else
+        // changed, ten calls in a graph, fp16 against fp32: one 2K row 17.2 us,
+        // 18.8; one 32K row 24.7, 26.8; two of 20K-30K 28.8, 32.6; eight of
+        // 4K-12K 34.4, 38.4.  (Tiles of up to 32 rows gain nothing and keep
+        // fp32: one 2K row of 16 heads 12.9, 12.5.)
+        // [column / 8][row][8] or [column / 4][row][4], so that a warp's stores
         // are whole lines.
         // Finished rows: 64 bytes of 16 rows at a time through shared memory,
         // so that four lanes write a row's piece.
         const int pm = p.tp * p.H;  // rows a partial has room for
-        uint4* const pout = p.part_o + part * pm * (kDV / 8) + h;
+        uint4* const pout = p.part_o + part * pm * (p.part_f32 ? kDV / 4 : kDV / 8) + h;
         const int elt = p.out_bf16 ? 2 : 4;
         uint8_t* const gout =
             reinterpret_cast<uint8_t*>(p.out) + ((int64_t)wk.q0 + (warp & 3) * 32) * (int64_t)(kDV * elt);
@@ -761,7 +766,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
           }
           if (!whole) {
-            if (h < wk.m) {
+            if (h < wk.m && p.part_f32) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                pout[(int64_t)(c0 / 4 + c) * pm] = make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+            } else if (h < wk.m) {
               float big = 0.f;
 #pragma unroll
               for (int c = 0; c < 32; ++c) big = fmaxf(big, fabsf(__uint_as_float(ov[c])));
@@ -773,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   if (v < INFINITY) big = fmaxf(big, v);
                 }
               }
-              const int e = partial_exponent(big);
+              const int e = min(max((int)(__float_as_uint(big) >> 23), 1), 253);  // biased exponent
               const float scale = __uint_as_float((uint32_t)(254 - e) << 23);
               p.part_sc[(part * (kDV / 32) + c0 / 32) * pm + h] = __uint_as_float((uint32_t)e << 23);  // 1 / scale
 #pragma unroll
@@ -848,13 +857,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // way round.
 constexpr int kMaxWorkers = 256;
 
-template <int SPLIT, int WARPS>
+template <int SPLIT, int WARPS, bool F32>
 __global__ void __launch_bounds__(32 * WARPS)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
                              const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_workers, int pm,
                              void* out, int out_bf16, float* lse) {
   constexpr int kGroups = WARPS / SPLIT;  // column groups per task
   constexpr int kFlight = 8;              // partials a thread has in flight
+  constexpr int kVec = F32 ? 2 : 1;       // 16-byte pieces of eight columns
   __shared__ CutRow s_cut[kMaxWorkers];
   __shared__ int s_count[WARPS];
   __shared__ float s_sum[SPLIT > 1 ? WARPS : 1][10][32];
@@ -885,21 +895,24 @@ __global__ void __launch_bounds__(32 * WARPS)
     float M = -INFINITY, l = 0.f;
     if (h < c.m) {
       for (int i0 = sub; i0 < c.count; i0 += SPLIT * kFlight) {
-        uint4 o[kFlight];
+        uint4 o[kFlight][kVec];
         float m[kFlight], li[kFlight], sc[kFlight], top = M;
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int i = i0 + SPLIT * k;
           m[k] = -INFINITY;
-          li[k] = sc[k] = 0.f;
-          o[k] = make_uint4(0u, 0u, 0u, 0u);
+          li[k] = 0.f;
+          sc[k] = F32 ? 1.f : 0.f;
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) o[k][v] = make_uint4(0u, 0u, 0u, 0u);
           if (i < c.count) {
             // the first partial is its cluster's second, the others are their clusters' first
             const int64_t part = 2 * (int64_t)(c.first + i) + (i == 0 ? 1 : 0);
             m[k] = __ldg(part_ml + 2 * part * pm + h);
             li[k] = __ldg(part_ml + (2 * part + 1) * pm + h);
-            sc[k] = __ldg(part_sc + (part * (kDV / 32) + grp / 4) * pm + h);
-            o[k] = __ldg(part_o + (part * (kDV / 8) + grp) * pm + h);
+            if (!F32) sc[k] = __ldg(part_sc + (part * (kDV / 32) + grp / 4) * pm + h);
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) o[k][v] = __ldg(part_o + (part * (kDV / 8) * kVec + grp * kVec + v) * pm + h);
           }
         }
 #pragma unroll
@@ -914,12 +927,19 @@ __global__ void __launch_bounds__(32 * WARPS)
         for (int k = 0; k < kFlight; ++k) {
           const float w = exp2f(m[k] - off), ws = w * sc[k];
           l = fmaf(w, li[k], l);
-          const uint32_t w4[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
-            acc[2 * e] = fmaf(ws, f.x, acc[2 * e]);
-            acc[2 * e + 1] = fmaf(ws, f.y, acc[2 * e + 1]);
+          for (int v = 0; v < kVec; ++v) {
+            const uint32_t w4[4] = {o[k][v].x, o[k][v].y, o[k][v].z, o[k][v].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (F32) {
+                acc[4 * v + e] = fmaf(ws, __uint_as_float(w4[e]), acc[4 * v + e]);
+              } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+                acc[2 * e] = fmaf(ws, f.x, acc[2 * e]);
+                acc[2 * e + 1] = fmaf(ws, f.y, acc[2 * e + 1]);
+              }
+            }
           }
         }
       }
@@ -1012,7 +1032,8 @@ int paged_workers(int T, int H) { return few_rows(T, H) ? paged_few_workers() : 
 
 size_t paged_workspace(int T, int H) {
   const size_t n = (size_t)paged_workers(T, H), m = (size_t)tokens_per_tile(T, H) * H;
-  return n * sizeof(CutRow) + 2 * n * m * kDV * sizeof(__half) + 2 * n * m * (2 + kDV / 32) * sizeof(float);
+  // (fp32 partials and no scales: more than fp16 ones with theirs)
+  return n * sizeof(CutRow) + 2 * n * m * (2 + kDV) * sizeof(float);
 }
 
 }  // namespace
@@ -1057,8 +1078,9 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.lse = lse;
   p.cut = reinterpret_cast<CutRow*>(workspace);
   const size_t pm = (size_t)p.tp * H;
+  p.part_f32 = few_rows(T, H) || !p.out_bf16 ? 1 : 0;
   p.part_o = reinterpret_cast<uint4*>(p.cut + n);
-  p.part_ml = reinterpret_cast<float*>(p.part_o + 2 * n * pm * (kDV / 8));
+  p.part_ml = reinterpret_cast<float*>(p.part_o + 2 * n * pm * (p.part_f32 ? kDV / 4 : kDV / 8));
   p.part_sc = p.part_ml + 2 * n * pm * 2;
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
@@ -1098,10 +1120,14 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
     const int warps = std::max(split, 8), groups = warps / split;  // column groups per task
     const int64_t tasks = (int64_t)std::min(p.n_rows, n - 1) * (((int64_t)pm + 31) / 32) * (kDV / 8 / groups);
     const dim3 grid((unsigned)std::min<int64_t>(tasks, 8 * (int64_t)device_info().sm_count)), block(32 * warps);
-    const auto kernel = split == 16  ? paged_mla_combine_kernel<16, 16>
-                        : split == 8 ? paged_mla_combine_kernel<8, 8>
-                        : split == 4 ? paged_mla_combine_kernel<4, 8>
-                                     : paged_mla_combine_kernel<1, 8>;
+    const auto pick = [split](auto f32) {
+      constexpr bool kF32 = decltype(f32)::value;
+      return split == 16  ? paged_mla_combine_kernel<16, 16, kF32>
+             : split == 8 ? paged_mla_combine_kernel<8, 8, kF32>
+             : split == 4 ? paged_mla_combine_kernel<4, 8, kF32>
+                          : paged_mla_combine_kernel<1, 8, kF32>;
+    };
+    const auto kernel = p.part_f32 ? pick(std::true_type{}) : pick(std::false_type{});
     if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float*)p.part_sc, (const uint4*)p.part_o,
                    n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
       return DSA_ERR_CUDA;

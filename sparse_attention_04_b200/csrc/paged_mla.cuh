@@ -42,8 +42,11 @@ struct PagedMlaParams {
   float* lse;
   CutRow* cut;       // [n_workers]
   float* part_ml;    // [2 * n_workers][2][tp * H]: maximum, sum
-  float* part_sc;    // [2 * n_workers][16][tp * H]: what 32 columns are to be multiplied by
-  uint4* part_o;     // [2 * n_workers][64][tp * H][8] fp16, unnormalised
+  // unnormalised, in 16-byte pieces: [2 * n_workers][128][tp * H][4] fp32 or,
+  // from the CTA pair with bf16 output, [2 * n_workers][64][tp * H][8] fp16
+  uint4* part_o;
+  float* part_sc;    // [2 * n_workers][16][tp * H]: what 32 columns of fp16 are to be multiplied by
+  int part_f32;
   int32_t* status;
   int debug_stall;
   uint64_t wait_limit_ns;
@@ -228,12 +231,6 @@ __device__ __forceinline__ MlaWalk<CHUNK, UNITS> first_part(const PagedMlaParams
   wk.r_seq = p.tiles == 1 ? wk.r : wk.r / p.tiles;
   wk.r_tile = wk.r - wk.r_seq * p.tiles;
   return wk;
-}
-
-// The scale of a partial's 32 columns: the biased exponent of the largest
-// finite one, so that the largest comes to [1, 2).
-__device__ __forceinline__ int partial_exponent(float big) {
-  return min(max((int)(__float_as_uint(big) >> 23), 1), 253);
 }
 
 // The kernel for tiles of up to kFewRows rows, one CTA per worker.

@@ -26,7 +26,7 @@
 // pair of paged_mla.cu: 117; a ring of eight pieces: 98); 32 sequences of 8K to
 // 128K slots, 16 heads: 465 of 451.  A chunk takes about 3400 cycles, 1350 of
 // them in the consumers; without loads the first case takes 76.  The rest is
-// latency at both ends: one row of 2K takes 12.7 us, one of 32K 17.4 (16 heads,
+// latency at both ends: one row of 2K takes 12.5 us, one of 32K 17.2 (16 heads,
 // ten calls in a graph).
 #include "paged_mla.cuh"
 #include "tmap.h"
@@ -567,27 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   o[1] = v[1];
                 }
               }
-            } else {
-              // fp16, each row's 32 columns scaled by their largest finite one: 11 bits
-              // against the 8 that P has, and half the bytes of fp32
-              float big = 0.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float t = fabsf(w[e]);
-                if (t < INFINITY) big = fmaxf(big, t);
-              }
-              big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-              big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-              const int e2 = partial_exponent(big);
-              const float scale = __uint_as_float((uint32_t)(254 - e2) << 23);
-              if (r < wk.m) {
-                uint4 o;
-                __half2* const t = reinterpret_cast<__half2*>(&o);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) t[e] = __floats2half2_rn(w[2 * e] * scale, w[2 * e + 1] * scale);
-                p.part_o[(part * (kDV / 8) + col / 8 + sub) * pm + r] = o;
-                if (sub == 0) p.part_sc[(part * (kDV / 32) + col / 32) * pm + r] = __uint_as_float((uint32_t)e2 << 23);
-              }
+            } else if (r < wk.m) {
+              uint4* const o = p.part_o + (part * (kDV / 4) + col / 4 + 2 * sub) * pm + r;
+              o[0] = *reinterpret_cast<const uint4*>(&v[0]);
+              o[pm] = *reinterpret_cast<const uint4*>(&v[1]);
             }
           }
           __syncwarp();

@@ -1,0 +1,57 @@
+"""More of the paged operators on the GPU: what their answers must not depend on,
+sizes at the limits of the interface, bad pages in every part of a call."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 192 ** -0.5
+U = 2.0 ** -24
+D, DV = 576, 512
+
+
+def _lib():
+    from sparse_attention_04_b200 import _lib as L
+    return L
+
+
+def _attend(q, kv, table, lens, out_dtype=torch.float32, scale=SCALE):
+    L, (B, T, H, _) = _lib(), q.shape
+    out = torch.full((B, T, H, DV), float("nan"), dtype=out_dtype, device=q.device)
+    lse = torch.full((B, T, H), float("nan"), device=q.device)
+    ws = torch.full((max(16, L.paged_mla_workspace_size(B, T, H)),), 0xff, dtype=torch.uint8, device=q.device)
+    st = torch.zeros(1, dtype=torch.int32, device=q.device)
+    L.paged_mla(q, kv, table, lens, scale, out, lse=lse, workspace=ws, status=st)
+    torch.cuda.synchronize()
+    return out, lse, int(st.item())
+
+
+@pytest.mark.parametrize("H,T", [(128, 1), (40, 3), (16, 1), (16, 2), (1, 1)])
+@pytest.mark.parametrize("lens", [[2048], [20000, 300, 64, 5000], [9000] * 5])
+def test_fp32_output_keeps_fp32_sums(cuda_device, H, T, lens):
+    """A query of zeros weighs every slot alike: P = 1, and the sums of whole
+    numbers below 2^24 are exact in fp32 whatever their order, so that only the
+    reciprocal and the product with it round (u each; one more for the
+    reciprocal's own error).  Partial sums kept in fewer bits would show."""
+    g = torch.Generator(device=cuda_device).manual_seed(H)
+    per = [-(-n // 64) for n in lens]
+    kv = torch.randint(129, 256, (sum(per), 64, D), generator=g, device=cuda_device).to(torch.bfloat16)
+    table = torch.zeros(len(lens), max(per), dtype=torch.int32, device=cuda_device)
+    at = 0
+    for b, k in enumerate(per):
+        table[b, :k] = torch.arange(at, at + k, device=cuda_device)
+        at += k
+    q = torch.zeros(len(lens), T, H, D, dtype=torch.bfloat16, device=cuda_device)
+    out, lse, st = _attend(q, kv, table, torch.tensor(lens, dtype=torch.int32, device=cuda_device))
+    assert st == 0
+    for b, n_all in enumerate(lens):
+        rows = kv[table[b, :per[b]].long()].view(-1, D)[:n_all, :DV].double()
+        for t in range(T):
+            n = n_all - T + t + 1
+            assert n * 255 < 1 << 24
+            ref = rows[:n].mean(0).expand(H, DV)
+            err = (out[b, t].double() - ref).abs()
+            assert torch.all(err <= 3 * U * ref), (b, t, float((err / ref).max() / U))
+            assert torch.all((lse[b, t].double() - math.log(n)).abs() <= 8 * U * math.log(n))
