@@ -298,7 +298,9 @@ int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* pag
  * and scale as for dsa_sparse_mla):
  *   l_s = scale * q[b,t,h,:576] . kv(b,s)[:576],  s <= lens[b] - T + t;  p = softmax_s(l)
  *   out[b,t,h,:] = sum_s p_s * kv(b,s)[:512];  lse[b,t,h] = log sum_s exp(l_s)
- * Rows that see no slot get out = 0, lse = -inf.
+ * Rows that see no slot, or whose scores are all -inf, get lse = -inf and
+ * out = 0.  (A slot that holds infinities and has weight 0 gives NaN or 0 in
+ * their columns; a score of NaN or +inf gives NaN.)
  * The cache is read once per 128 (token, head) rows of a sequence.  The work
  * is divided by the lengths found on the device, so ragged batches need no
  * padding and no plan.  The result does not depend on what else runs; the same

@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(32 * WARPS)
     if (h >= c.m) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN among the scores stays one
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
+    for (int e = 0; e < 8; ++e) acc[e] *= inv;  // (as in a tile that nothing cuts: 0 * infinity is a NaN)
     const int64_t rh = (int64_t)c.q0 + h;
     if (out_bf16) {
       uint32_t w4[4];

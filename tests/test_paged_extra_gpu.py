@@ -55,3 +55,23 @@ def test_fp32_output_keeps_fp32_sums(cuda_device, H, T, lens):
             err = (out[b, t].double() - ref).abs()
             assert torch.all(err <= 3 * U * ref), (b, t, float((err / ref).max() / U))
             assert torch.all((lse[b, t].double() - math.log(n)).abs() <= 8 * U * math.log(n))
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [128, 40, 16])
+def test_rows_whose_weights_all_vanish_do_not_depend_on_the_split(cuda_device, H, out_dtype):
+    """Every score is -inf: lse = -inf, and out = sum 0 * v, NaN in the columns
+    that hold infinities and 0 in the others, whether a row is split or not."""
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    kv = torch.randn(16, 64, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    kv[..., 5] = float("-inf")
+    for B in (1, 3, 400):  # one row over the whole card, ..., whole rows
+        table = torch.arange(16, dtype=torch.int32, device=cuda_device).expand(B, 16).contiguous()
+        lens = torch.full((B,), 1000, dtype=torch.int32, device=cuda_device)
+        q = torch.zeros(B, 1, H, D, dtype=torch.bfloat16, device=cuda_device)
+        q[..., 5] = 1.0
+        out, lse, st = _attend(q, kv, table, lens, out_dtype)
+        assert st == 0 and torch.all(lse == float("-inf"))
+        assert torch.isnan(out[..., 5]).all(), B
+        out[..., 5] = 0
+        assert torch.all(out == 0), B
