@@ -233,12 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ropes > 0) mbar_wait(bar(kRopeFull), (ropes - 1) & 1, &never, 10000000ull);
     }
   } else if (warp == kQueryWarp) {
-    // ---- the query, once no product reads the one before
+    // ---- the query, once no product reads the one before.  That takes as long
+    // as the part before does, so the limit is one per chunk of it.  (A chunk
+    // that does not come ends the other warps' waits, and with them this one.)
     const uint32_t on = elect_one();
     uint32_t item = 0;
+    uint64_t limit = 0;
     while (wk.next(p)) {
       if (wk.lo >= wk.hi) continue;
-      if (item > 0 && !wait(kQFree, (item - 1) & 1)) break;
+      if (item > 0 && !warp_wait(bar(kQFree), (item - 1) & 1, abort, limit)) break;
+      limit = p.wait_limit_ns * (uint64_t)(wk.hi - wk.lo + 1);
       if (on) {
         mbar_arrive_expect_tx(bar(kQFull), kKB * L::kQBlockBytes);
         for (int kb = 0; kb < kKB; ++kb) tma_load_2d(sbase + L::kQOff + kb * L::kQBlockBytes, &tm_q, kb * 64, wk.q0, bar(kQFull));

@@ -75,3 +75,23 @@ def test_rows_whose_weights_all_vanish_do_not_depend_on_the_split(cuda_device, H
         assert torch.isnan(out[..., 5]).all(), B
         out[..., 5] = 0
         assert torch.all(out == 0), B
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_two_sequences_of_a_billion_slots(cuda_device, H):
+    """Page lists that name the same pages again and again: a worker's part takes
+    longer than one wait may.  Zero scores: out is the mean of rows of ones,
+    lse = log n.  An accumulator takes a chunk's sum at a time, 2^18 of them here,
+    each addition off by 2u: 2^-5."""
+    free, _ = torch.cuda.mem_get_info()
+    n, P = (1 << 30) + 64 * 1000, 64
+    if free < 8 * n // P * 4:
+        pytest.skip("needs room for the page lists")
+    table = (torch.arange(n // P, dtype=torch.int32, device=cuda_device) % 1024).expand(2, -1).contiguous()
+    kv = torch.ones(1024, P, D, dtype=torch.bfloat16, device=cuda_device)
+    lens = torch.full((2,), n, dtype=torch.int32, device=cuda_device)
+    q = torch.zeros(2, 1, H, D, dtype=torch.bfloat16, device=cuda_device)
+    out, lse, st = _attend(q, kv, table, lens)
+    assert st == 0
+    assert torch.all((out - 1).abs() <= 2.0 ** -5)
+    assert torch.all((lse - math.log(n)).abs() <= 2.0 ** -5)
