@@ -1084,7 +1084,9 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
   p.part_sc = p.part_ml + 2 * n * pm * 2;
   p.status = dev_status;
   p.debug_stall = debug.debug_stall;
-  p.wait_limit_ns = debug.wait_limit_ns;
+  // A worker may write any number of empty tiles while its other warps wait for
+  // it: 2 us each with one head, 5 with 128 (2^24 empty rows of one head: 0.23 s).
+  p.wait_limit_ns = debug.wait_limit_ns + (debug.debug_stall ? 0 : 10000ull * (uint64_t)p.n_rows);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t rows = (uint64_t)n_pages * page_size;
   if (few_rows(T, H)) {

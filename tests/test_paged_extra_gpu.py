@@ -95,3 +95,25 @@ def test_two_sequences_of_a_billion_slots(cuda_device, H):
     assert st == 0
     assert torch.all((out - 1).abs() <= 2.0 ** -5)
     assert torch.all((lse - math.log(n)).abs() <= 2.0 ** -5)
+
+
+def test_a_batch_of_16_million_mostly_empty_sequences(cuda_device):
+    """The largest batch: a worker writes 113 K empty rows before it comes to a
+    chunk that its other warps have long been waiting for."""
+    L, B = _lib(), 1 << 24
+    free, _ = torch.cuda.mem_get_info()
+    if free < B * 2 * (D + DV) + (4 << 30):
+        pytest.skip("needs 41 GB")
+    kv = torch.ones(16, 64, D, dtype=torch.bfloat16, device=cuda_device)
+    table = torch.arange(16, dtype=torch.int32, device=cuda_device).expand(B, 16)[:, :11].contiguous()
+    lens = torch.zeros(B, dtype=torch.int32, device=cuda_device)
+    lens[-1], lens[1000] = 700, 1
+    q = torch.zeros(B, 1, 1, D, dtype=torch.bfloat16, device=cuda_device)
+    out = torch.full((B, 1, 1, DV), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    ws = torch.empty(L.paged_mla_workspace_size(B, 1, 1), dtype=torch.uint8, device=cuda_device)
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    L.paged_mla(q, kv, table, lens, SCALE, out, workspace=ws, status=st)
+    assert int(st.item()) == 0
+    assert torch.all(out[-1] == 1) and torch.all(out[1000] == 1)
+    out[-1], out[1000] = 0, 0
+    assert not out.view(torch.int32).any()
