@@ -193,10 +193,12 @@ def copy_device_to_host(dst_host, src, stream=None):
     _check(lib.dsa_copy_device_to_host(_host_p(dst_host), _p(src), n, _stream(stream)), "dsa_copy_device_to_host")
 
 
-def debug_stall_attention(n_launches: int, wait_limit_ns: int = 0):
+def debug_stall_attention(n_launches: int, wait_limit_ns: int = 0, at_product: bool = False):
     """dsa_debug_stall_attention: the next n_launches attention launches take
-    their timeout path after wait_limit_ns (a test hook)."""
-    _check(lib.dsa_debug_stall_attention(n_launches, wait_limit_ns), "dsa_debug_stall_attention")
+    their timeout path after wait_limit_ns (a test hook); at_product: in the
+    middle of the paged attention's work."""
+    _check(lib.dsa_debug_stall_attention(n_launches | (1 << 30 if at_product else 0), wait_limit_ns),
+           "dsa_debug_stall_attention")
 
 
 def decode_step_launches(B, max_end_pos, k, H) -> int:

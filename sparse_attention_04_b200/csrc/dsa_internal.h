@@ -123,9 +123,10 @@ struct MlaParams {
   int32_t* status;
   int early_inputs;  // q and offsets may be read before the dependency wait
   int dense;         // no index list: row r attends to its whole causal prefix
-  // Test hook (dsa_debug_stall_attention): 1 makes the query barrier expect
-  // one arrival more than will ever come, so its wait runs out and the
-  // kernel takes its timeout path.  0 in normal use.
+  // Test hook (dsa_debug_stall_attention): the query barrier expects this many
+  // arrivals more than will ever come, so its wait runs out and the kernel
+  // takes its timeout path.  (2 in the paged attention's CTA pair: the first
+  // message's barrier instead.)  0 in normal use.
   int debug_stall;
   uint64_t wait_limit_ns;  // limit of every pipeline wait (kWaitLimitNs in normal use)
 };

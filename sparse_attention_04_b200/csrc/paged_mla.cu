@@ -116,15 +116,53 @@ enum Bar : int {
 constexpr int kMiscOff = kBarOff + kNumBar * 8;
 struct Misc {
   int tmem_base, abort;
+  // what a CTA's warps have done when they are through, for settle():
+  uint32_t sent[2];  // CTA 0: messages that each sender warp has stored
+  uint32_t issued;   // CTA 1: messages whose product is committed
+  uint32_t armed;    // CTA 1: messages expected
   MlaScan<kThreads> scan;
 };
 constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBarOff % 8 == 0 && kMiscOff % 8 == 0 && kMsgBytes % 16 == 0 && kStageOff % 128 == 0 && kPOff % 128 == 0, "alignment");
+// Pieces of a message are dealt out to the sender's threads one by one: bytes
+// that its warp w stores.
+constexpr int kPieces = (int)kMsgBytes / 16;
+constexpr uint32_t sender_bytes(int w) {
+  const int rest = kPieces % kSendThreads - 32 * w;
+  return 16u * (uint32_t)(kPieces / kSendThreads * 32 + (rest < 0 ? 0 : rest > 32 ? 32 : rest));
+}
+static_assert(kSendThreads == 64 && sender_bytes(0) + sender_bytes(1) == kMsgBytes, "two sender warps");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // CTA 0: query blocks 0-7 in [0, 256), S buffers at 256 and 384
 constexpr uint32_t kIdescQK = idesc_bf16(128, kChunk);
 constexpr uint32_t kIdescPV = idesc_bf16(128, 256, /*b_mn_major=*/true);
+
+// After a timeout, when all warps of both CTAs are done: what the partner still
+// has on its way into this CTA's shared memory must land before the CTA exits.
+// One thread; every wait ends after 10 ms at most.
+__device__ __noinline__ void settle(uint32_t rank, uint32_t bars, const Misc* misc, uint32_t peer_misc) {
+  volatile int never = 0;
+  if (rank == 0) {  // arrivals of CTA 1's products
+    const uint32_t n = ld_cluster_u32(peer_misc + (uint32_t)offsetof(Misc, issued));
+    for (uint32_t k = n > kPBufs ? n - kPBufs : 0; k < n; ++k)
+      mbar_wait(bars + 8u * (kPvDone + k % kPBufs), (k / kPBufs) & 1, &never, 10000000ull);
+    return;
+  }
+  // Messages, the last three at most: one is sent when the product of the third
+  // before it is complete.  A sender warp may have given up before the other,
+  // and the message may not be expected yet.
+  const uint32_t sent0 = ld_cluster_u32(peer_misc + (uint32_t)offsetof(Misc, sent));
+  const uint32_t sent1 = ld_cluster_u32(peer_misc + (uint32_t)offsetof(Misc, sent) + 4u);
+  const uint32_t n = max(sent0, sent1);
+  for (uint32_t k = n > kPBufs ? n - kPBufs : 0; k < n; ++k) {
+    const uint32_t full = bars + 8u * (kPFull + k % kPBufs);
+    if (k >= misc->armed) mbar_arrive_expect_tx(full, kMsgBytes);
+    if (k >= sent0) mbar_complete_tx(full, sender_bytes(0));
+    if (k >= sent1) mbar_complete_tx(full, sender_bytes(1));
+    mbar_wait(full, (k / kPBufs) & 1, &never, 10000000ull);
+  }
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -137,10 +175,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort = &misc->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const uint32_t peer_abort = mapa_shared(sbase + kMiscOff + (uint32_t)offsetof(Misc, abort), rank ^ 1u);
+  const uint32_t peer_misc = mapa_shared(sbase + kMiscOff, rank ^ 1u);
   auto give_up = [&]() {
     *abort = 1;
-    st_cluster_u32(peer_abort, 1u);
+    st_cluster_u32(peer_misc + (uint32_t)offsetof(Misc, abort), 1u);
   };
 
   // ---- prologue: barriers, TMEM
@@ -149,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(rank == 0 ? &tm_k : &tm_v);
       if (rank == 0) tma_prefetch_desc(&tm_q);
-      mbar_init(bar(kQFull), 1 + p.debug_stall);
+      mbar_init(bar(kQFull), 1 + (p.debug_stall & 1));
       mbar_init(bar(kQFree), 1);
       for (int i = 0; i < kKSlots; ++i) {
         mbar_init(bar(kKFull + i), 1);
@@ -167,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPBufs; ++i) {
         mbar_init(bar(kPvDone + i), 1);
         mbar_init(bar(kPFull + i), 1);
-        mbar_init(bar(kReady + i), 8);
+        mbar_init(bar(kReady + i), 8 + (i == 0 ? p.debug_stall >> 1 : 0));
       }
       for (int i = 0; i < kVSlots; ++i) {
         mbar_init(bar(kVFull + i), 1);
@@ -373,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t rem_msg = mapa_shared(sbase + kPOff, 1);
       const uint32_t rem_pfull = mapa_shared(bar(kPFull), 1);
       const int tid = threadIdx.x - kSendWarp * 32;
-      constexpr int kPieces = (int)kMsgBytes / 16, kBatch = 9;
+      constexpr int kBatch = 9;
       static_assert(kPieces <= 2 * kBatch * kSendThreads, "two rounds per message");
       uint32_t j = 0;
       bool ok = true;
@@ -405,14 +443,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // CTA 1's last arrivals here must land before this CTA exits
       for (uint32_t k = j > kPBufs ? j - kPBufs : 0; ok && k < j; ++k)
         ok = warp_wait<true>(bar(kPvDone + k % kPBufs), (k / kPBufs) & 1, abort, p.wait_limit_ns);
-      if (*abort) {
-        give_up();
-        // nobody here can see the last stores land in the partner: 50 us are
-        // ample, and the partner does not leave before this CTA
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 50000ull) {
-        }
-      }
+      if (lane == 0) misc->sent[warp - kSendWarp] = j;
+      if (*abort) give_up();
     } else if (warp < 8) {
       // ---- softmax: thread = (head h, slots 64 * half .. of every chunk)
       const int h = (warp & 3) * 32 + lane, half = warp >> 2;
@@ -581,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return there;
       };
-      uint32_t j = 0, ring = 0;
+      uint32_t j = 0, ring = 0, issued = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
         for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
@@ -600,8 +632,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (on) tc_commit(bar(kVEmpty + slot));
           }
           if (ok && on) tc_commit_mc(bar(kPvDone + pb), 0x3);
+          if (ok) ++issued;
         }
       }
+      if (lane == 0) misc->issued = issued;
       if (*abort) {
         give_up();
         volatile int never = 0;
@@ -614,15 +648,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- expects message j in buffer j % 3 once that buffer is free.  (Done
       // here and not by the sender: an arrival on another CTA's barrier
       // releases the thread's earlier stores first, which took 2000 cycles.)
-      uint32_t j = 0;
+      uint32_t j = 0, armed = 0;
       bool ok = true;
       while (ok && wk.next(p)) {
         for (int i = 2 * wk.lo; ok && i < 2 * wk.hi; ++i, ++j) {
           const uint32_t pb = j % kPBufs;
           ok = j < kPBufs || warp_wait(bar(kPvDone + pb), ((j / kPBufs) - 1) & 1, abort, p.wait_limit_ns);
           if (ok && lane == 0) mbar_arrive_expect_tx(bar(kPFull + pb), kMsgBytes);
+          if (ok) ++armed;
         }
       }
+      if (lane == 0) misc->armed = armed;
       if (*abort) give_up();
     } else if (warp < 8) {
       // ---- rescale and epilogue: thread = (head h, half of the columns)
@@ -841,6 +877,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   // neither CTA leaves while the other may still write into its shared memory
   cluster_sync_all();
+  if (*abort) {  // the same in both CTAs: whoever gives up tells the partner
+    if (threadIdx.x == 0) settle(rank, bar(0), misc, peer_misc);
+    __syncwarp();
+    cluster_sync_all();  // the partner has read this CTA's counts
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

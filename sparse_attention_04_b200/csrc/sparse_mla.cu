@@ -744,6 +744,7 @@ size_t mla_workspace_bytes(int n_rows, int H, int k) {
 
 namespace {
 std::atomic<int> g_stall_left{0};
+std::atomic<int> g_stall_kind{1};
 std::atomic<uint64_t> g_stall_limit_ns{0};
 }  // namespace
 
@@ -754,7 +755,7 @@ void take_attention_debug(MlaParams& p) {
   while (left > 0 && !g_stall_left.compare_exchange_weak(left, left - 1)) {
   }
   if (left > 0) {
-    p.debug_stall = 1;
+    p.debug_stall = g_stall_kind.load();
     p.wait_limit_ns = g_stall_limit_ns.load();
   }
 }
@@ -825,8 +826,11 @@ int launch_sparse_mla(const MlaArgs& a, cudaStream_t stream) {
 
 extern "C" int dsa_debug_stall_attention(int n_launches, uint64_t wait_limit_ns) {
   if (n_launches < 0) return DSA_ERR_INVALID_ARG;
+  const int kind = n_launches & DSA_STALL_AT_PRODUCT ? 2 : 1;
+  n_launches &= ~DSA_STALL_AT_PRODUCT;
   if (n_launches > 0 && (wait_limit_ns < 1000000ull || wait_limit_ns > 1000000000ull)) return DSA_ERR_INVALID_ARG;
   dsa::g_stall_limit_ns.store(wait_limit_ns);
+  dsa::g_stall_kind.store(kind);
   dsa::g_stall_left.store(n_launches);
   return DSA_OK;
 }

@@ -117,3 +117,27 @@ def test_a_batch_of_16_million_mostly_empty_sequences(cuda_device):
     assert torch.all(out[-1] == 1) and torch.all(out[1000] == 1)
     out[-1], out[1000] = 0, 0
     assert not out.view(torch.int32).any()
+
+
+@pytest.mark.parametrize("H,T", [(128, 1), (20, 5)])
+@pytest.mark.parametrize("lens", [[100], [60000, 7000], [3000, 40, 0, 700]])
+def test_a_wait_that_runs_out_in_mid_stream_then_the_next_call_is_right(cuda_device, H, T, lens):
+    """The test hook holds back the first product with the values: messages
+    between the CTAs are under way when the waits run out."""
+    L, B = _lib(), len(lens)
+    g = torch.Generator(device=cuda_device).manual_seed(4)
+    per = max(-(-n // 64) for n in lens)
+    kv = torch.randn(B * per, 64, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    table = torch.arange(B * per, dtype=torch.int32, device=cuda_device).view(B, per)
+    q = torch.randn(B, T, H, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    want = _attend(q, kv, table, n)
+    assert want[2] == 0
+    L.debug_stall_attention(3, 2_000_000, at_product=True)
+    try:
+        assert [_attend(q, kv, table, n)[2] for _ in range(3)] == [5, 5, 5]
+    finally:
+        L.debug_stall_attention(0, 0)
+    for _ in range(2):
+        out, lse, st = _attend(q, kv, table, n)
+        assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
