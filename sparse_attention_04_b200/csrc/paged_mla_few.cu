@@ -89,6 +89,11 @@ struct Layout {
   static constexpr int kSmemBytes = kMiscOff + (int)sizeof(Misc) + 1024;
   // The 128 product rows of the last block end inside shared memory: P and Q
   // lie behind it.  The epilogue stages 2 KB per warp where P was.
+  // Fewer places than three chunks have pieces: the scores of chunk g + 2 are
+  // computed only after the product of chunk g has freed a piece, that is after
+  // all eight consumer warps saw chunk g's scores.  Four of them alone give a
+  // score buffer back; the others would miss a phase of its barrier otherwise.
+  static_assert(kRing < 3 * kPieces, "a score buffer filled twice behind a waiting warp");
   static_assert(kRing <= kMaxRing && kRing >= 2 * kPieces && kSmemBytes <= 232448 && 2 * kPBytes >= 8 * 2048, "shared memory budget");
   static_assert(kQOff % 1024 == 0 && kMaxOff % 16 == 0 && kAlphaOff % 16 == 0 && kBarOff % 8 == 0 && kMiscOff % 8 == 0,
                 "alignment");
