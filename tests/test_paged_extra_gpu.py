@@ -141,3 +141,62 @@ def test_a_wait_that_runs_out_in_mid_stream_then_the_next_call_is_right(cuda_dev
     for _ in range(2):
         out, lse, st = _attend(q, kv, table, n)
         assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("P,H,T", [(64, 100, 3), (16, 128, 2), (48, 7, 1), (128, 128, 1), (32, 16, 20)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_weights_beside_bad_pages_by_definition(cuda_device, P, H, T, in_place):
+    """Slots on bad pages get decay * acc and count in nothing else, over every
+    query tile of a sequence (up to three here)."""
+    from test_paged_gpu import Cache, _attend as attend, _factor, _q
+
+    class Holed(Cache):
+        """Rows by the page lists as they were."""
+
+        def rows(self, b, slots):
+            return getattr(self, "good", self.table)[b].long()[slots // self.P] * self.P + slots % self.P
+
+    lens = [700, 3 * P, 0, P, 5000, T]
+    c = Holed(cuda_device, lens, P, seed=P + T)
+    c.good = c.table.clone()
+    bad = {0: [1, (700 - 1) // P], 1: [0, 1, 2], 3: [0], 4: [0, 7, 8, 4999 // P]}
+    for b, pages in bad.items():
+        for i in pages:
+            c.table[b, i] = (-1, c.kv.shape[0], -(1 << 31), (1 << 31) - 1)[i % 4]
+
+    def skip(b):
+        s = torch.zeros(lens[b], dtype=torch.bool, device=c.dev)
+        for i in bad.get(b, []):
+            s[P * i:P * i + P] = True
+        return s
+
+    q = _q(c, len(lens), T, H)
+    _, lse, st = attend(c, q)
+    assert st == 6
+    acc = torch.rand(len(lens), 5008, generator=c.g, device=c.dev)
+    before = acc.clone()
+    out = acc if in_place else torch.full_like(acc, -7.0)
+    status = torch.zeros(1, dtype=torch.int32, device=c.dev)
+    _lib().paged_weights(q, c.kv, c.table, c.lens, lse, SCALE, acc, acc_out=None if in_place else out, decay=0.75,
+                         status=status)
+    assert int(status.item()) == 6
+    for b, n_all in enumerate(lens):
+        k, ref = c.of(b), before[b, :n_all].double() * 0.75
+        tol = 4 * U * ref.abs()
+        for t in range(T):
+            n = max(0, n_all - T + t + 1)
+            rows = ~torch.isinf(lse[b, t])  # the others saw nothing
+            if n == 0 or not bool(rows.any()):
+                assert n == 0 or bool(skip(b)[:n].all())
+                continue
+            qq, L = q[b, t].double()[rows], lse[b, t].double()[rows]
+            x = SCALE * (qq @ k[:n].T)
+            w = (x - L[:, None]).exp() * (~skip(b)[:n])
+            # a logit as in the attention's tests, its exponent, and the sum over the rows
+            f = _factor(SCALE, k[:n], qq, x) + 8 * U * L.abs()[:, None] + H * T * 2 * U
+            ref[:n] += w.sum(0)
+            tol[:n] += (w * f).sum(0) * 1.01
+        err = (out[b, :n_all].double() - ref).abs()
+        assert torch.all(err <= tol + 4 * U * ref.abs() + 1e-30), (b, float((err / (tol + 1e-30)).max()))
+        assert torch.equal(out[b, :n_all][skip(b)], before[b, :n_all][skip(b)] * 0.75), b
+        assert torch.equal(out[b, n_all:], before[b, n_all:] if in_place else torch.full_like(before[b, n_all:], -7.0)), b
