@@ -200,3 +200,32 @@ def test_weights_beside_bad_pages_by_definition(cuda_device, P, H, T, in_place):
         assert torch.all(err <= tol + 4 * U * ref.abs() + 1e-30), (b, float((err / (tol + 1e-30)).max()))
         assert torch.equal(out[b, :n_all][skip(b)], before[b, :n_all][skip(b)] * 0.75), b
         assert torch.equal(out[b, n_all:], before[b, n_all:] if in_place else torch.full_like(before[b, n_all:], -7.0)), b
+
+
+@pytest.mark.parametrize("ld,budget,recent", [(512, 100, 10), (70000, 30001, 500), (6 << 20, 3000001, 1000)])
+def test_plan_into_the_lengths_themselves_up_to_the_largest(cuda_device, ld, budget, recent):
+    """new_lens is lens; the largest row has almost no keys on chip."""
+    L = _lib()
+    g = torch.Generator(device=cuda_device).manual_seed(ld)
+    B = 2
+    acc = torch.randint(0, max(4, ld // 3), (B, ld), generator=g, device=cuda_device).float()  # with ties
+    pos = torch.stack([torch.randperm(ld, generator=g, device=cuda_device) for _ in range(B)]).to(torch.int32)
+    old = [ld, ld - 77]
+    lens = torch.tensor(old, dtype=torch.int32, device=cuda_device)
+    end = torch.full((B,), ld, dtype=torch.int32, device=cuda_device)
+    n_moves = torch.empty_like(lens)
+    dst = torch.empty(B, budget, dtype=torch.int32, device=cuda_device)
+    src, st = torch.empty_like(dst), torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    L.evict_plan(acc, pos, lens, end, budget, recent, lens, n_moves, dst, src, status=st)
+    assert int(st.item()) == 0 and lens.tolist() == [budget] * B
+    for b, n in enumerate(old):
+        order = acc[b, :n].argsort(descending=True, stable=True)
+        kept_always = pos[b, :n] >= ld - recent
+        order = order[kept_always[order].int().argsort(descending=True, stable=True)]
+        keep = torch.zeros(n, dtype=torch.bool, device=cuda_device)
+        keep[order[:budget]] = True
+        holes, tail = (~keep[:budget]).nonzero()[:, 0], budget + keep[budget:].nonzero()[:, 0]
+        m = int(n_moves[b])
+        assert m == len(holes) == len(tail)
+        assert torch.equal(dst[b, :m].long(), holes) and torch.equal(src[b, :m].long(), tail)
+        assert torch.all(dst[b, m:] == -1) and torch.all(src[b, m:] == -1)
