@@ -1150,8 +1150,11 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
       return DSA_ERR_CUDA;
   }
   if (n > 1) {
-    // Warps that share a row's partials, by how many a row has at most (one
-    // row of 32K: 30.9 us with eight, 33.0 with four, 37.0 with two; two rows
+    // Warps that share a row's partials, by how many a tile of the batch has on
+    // average (the lengths are known on the device only).  A batch of one long
+    // row among empty or short ones therefore gets too few: one 32K row takes
+    // 24.9 us alone and 35 to 41 among 63 others, with 16 heads 17.7 and 36.
+    // With rows of like length: (one row of 32K: 30.9 us with eight, 33.0 with four, 37.0 with two; two rows
     // 30.9, 28.9, 30.8; eight rows 51.5, 47.5, 43.5 and 42.8 with one, because
     // the tasks then fill the card several times over).  A tile of few rows has
     // few tasks, more warps fit beside one another (16 heads, back to back: one
