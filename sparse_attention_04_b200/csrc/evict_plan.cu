@@ -14,14 +14,14 @@
 // [r * S, (r + 1) * S).  The keys stay in shared memory as far as it goes, and
 // acc and pos are then read once (HBM bounds a large plan at 8 bytes per slot).
 // The bitmap has its place there too, a quarter byte per slot: all keys fit up
-// to about 47000 slots per CTA (ld_slots 370000 with eight CTAs), of 786432
+// to about 48600 slots per CTA (ld_slots 389000 with eight CTAs), of 786432
 // slots (DSA_MAX_PLAN_SLOTS) 2600 do.  The others are made again from acc and
 // pos where they are needed: these are read up to four times per search.
 //
 // B200: 32 sequences of 64K to 128K slots cut to 64K in 30 us (41 MB: 6.4 us of
-// HBM), eight of 4097 slots in 10.8 us (ten calls in a graph).  What bounds it is instruction issue and
-// about 30 barrier-separated steps: keys and first histogram 9 us, the digit
-// passes 10, bitmap and ranks 5, lists 6.
+// HBM), eight of 4097 slots in 10.8 us (ten calls in a graph).  What bounds it
+// is instruction issue and about 30 barrier-separated steps: keys and first
+// histogram 9 us, the digit passes 10, bitmap and ranks 5, lists 6.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
