@@ -34,8 +34,8 @@
 // inside the last box are zeroed in CTA 1 before the product (their P is 0,
 // but they may hold NaN) and masked in CTA 0.
 //
-// What bounds it (B200).  32 sequences of 8K to 128K slots, 128 heads: 0.54 ms
-// in a short run (4.3 TB/s, 1.03 PFLOP/s) and 0.64 ms in a long one, where the
+// What bounds it (B200).  32 sequences of 8K to 128K slots, 128 heads: 0.53 ms
+// in a short run (4.4 TB/s, 1.06 PFLOP/s) and 0.64 ms in a long one, where the
 // 1000 W cap holds the SM clock near 1.2 GHz; a chunk takes about 3400 cycles,
 // 2304 of them QK products.  Without the loads the same kernel takes 0.37 ms,
 // with all of them answered by L2 0.42 ms.  What the steps to it were worth:
@@ -45,7 +45,7 @@
 // the way of a message (it flushes the thread's earlier stores first, 2000
 // cycles) 0.70 -> 0.61.  Measured slower: requesting later chunks into L2 ahead
 // (0.55 -> 0.63 ms and more), P through the copy engine (behind the block loads
-// in its queue).  One 2K row takes 17.2 us and one 32K row 24.6, most of it
+// in its queue).  One 2K row takes 17.3 us and one 32K row 24.7, most of it
 // latency: query into TMEM, one chunk through both CTAs, the partial's stores,
 // the joining kernel.
 #include <cuda.h>
