@@ -316,7 +316,9 @@ int dsa_paged_append(const void* kv_new, const int32_t* lens, const int32_t* pag
  * fp16 (2^-11) before they are added up.
  * workspace: dsa_paged_mla_workspace_size(B, T, H) bytes, for the current
  * device; its contents need not survive between calls, and calls that may run
- * at the same time (two graphs, two streams) need one each.
+ * at the same time (two graphs, two streams) need one each.  Two that share one
+ * all the same give wrong results (reported as DSA_ERR_WORKSPACE where it
+ * shows), and touch nothing outside their own arrays.
  */
 size_t dsa_paged_mla_workspace_size(int B, int T, int H);
 int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table, int64_t ld_table, int max_pages,

@@ -902,7 +902,7 @@ template <int SPLIT, int WARPS, bool F32>
 __global__ void __launch_bounds__(32 * WARPS)
     paged_mla_combine_kernel(const CutRow* __restrict__ cut, const float* __restrict__ part_ml,
                              const float* __restrict__ part_sc, const uint4* __restrict__ part_o, int n_workers, int pm,
-                             void* out, int out_bf16, float* lse) {
+                             int64_t rows, void* out, int out_bf16, float* lse, int32_t* status) {
   constexpr int kGroups = WARPS / SPLIT;  // column groups per task
   constexpr int kFlight = 8;              // partials a thread has in flight
   constexpr int kVec = F32 ? 2 : 1;       // 16-byte pieces of eight columns
@@ -916,6 +916,14 @@ __global__ void __launch_bounds__(32 * WARPS)
   static_assert(kMaxWorkers <= 32 * WARPS, "a thread per worker");
   CutRow mine{-1, 0, 0, 0};
   if (threadIdx.x < n_workers) mine = cut[threadIdx.x];
+  // The only addresses that come out of the workspace.  Another call that uses
+  // it at the same time may have written them: no access outside this call's
+  // own arrays then.
+  if (mine.q0 >= 0 && (mine.m < 1 || mine.m > pm || mine.q0 > rows - mine.m || mine.first < 0 || mine.count < 1 ||
+                       mine.first > n_workers - mine.count)) {
+    mine.q0 = -1;
+    if (blockIdx.x == 0) report(status, DSA_ERR_WORKSPACE);
+  }
   const uint32_t cuts = __ballot_sync(0xffffffffu, mine.q0 >= 0);
   if (lane == 0) s_count[warp] = __popc(cuts);
   __syncthreads();
@@ -1175,7 +1183,7 @@ int dsa_paged_mla(const void* q, const void* kv_pages, const int32_t* page_table
     };
     const auto kernel = p.part_f32 ? pick(std::true_type{}) : pick(std::false_type{});
     if (launch_pdl(kernel, grid, block, 0, s, (const CutRow*)p.cut, (const float*)p.part_ml, (const float*)p.part_sc, (const uint4*)p.part_o,
-                   n, (int)pm, out, p.out_bf16, lse) != cudaSuccess)
+                   n, (int)pm, (int64_t)B * T * H, out, p.out_bf16, lse, dev_status) != cudaSuccess)
       return DSA_ERR_CUDA;
   }
   return DSA_OK;

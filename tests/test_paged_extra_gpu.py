@@ -229,3 +229,45 @@ def test_plan_into_the_lengths_themselves_up_to_the_largest(cuda_device, ld, bud
         assert m == len(holes) == len(tail)
         assert torch.equal(dst[b, :m].long(), holes) and torch.equal(src[b, :m].long(), tail)
         assert torch.all(dst[b, m:] == -1) and torch.all(src[b, m:] == -1)
+
+
+def test_two_overlapping_calls_that_share_a_workspace_stay_inside_their_arrays(cuda_device):
+    """A mistake of the caller: results are wrong, but nothing is read or written
+    outside, and the calls are right again one after the other."""
+    L = _lib()
+    g = torch.Generator(device=cuda_device).manual_seed(5)
+    jobs = []
+    kv = torch.randn(400, 64, D, generator=g, device=cuda_device).to(torch.bfloat16)
+    sizes = [([3000, 20, 0, 9000], 128, 1), ([25000], 16, 1), ([700] * 30, 40, 3)]
+    ws = torch.zeros(max(L.paged_mla_workspace_size(len(n), T, H) for n, H, T in sizes), dtype=torch.uint8, device=cuda_device)
+    for n, H, T in sizes:
+        B = len(n)
+        table = torch.randint(0, 400, (B, 400), generator=g, device=cuda_device, dtype=torch.int32)
+        q = torch.randn(B, T, H, D, generator=g, device=cuda_device).to(torch.bfloat16)
+        lens = torch.tensor(n, dtype=torch.int32, device=cuda_device)
+        want = _attend(q, kv, table, lens)
+        # guard rows before and behind out and lse
+        out = torch.full((3, B, T, H, DV), 7.0, device=cuda_device)
+        lse = torch.full((3, B, T, H), 7.0, device=cuda_device)
+        st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+        run = lambda q=q, table=table, lens=lens, out=out, lse=lse, st=st: L.paged_mla(
+            q, kv, table, lens, SCALE, out[1], lse=lse[1], workspace=ws, status=st)
+        s, cg = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(cg, stream=s):
+            for _ in range(10):
+                run()
+        jobs.append((s, cg, run, want, out, lse, st))
+    for _ in range(50):
+        for s, cg, *_rest in jobs:
+            with torch.cuda.stream(s):
+                cg.replay()
+    torch.cuda.synchronize()
+    for _, _, run, want, out, lse, st in jobs:
+        assert int(st.item()) in (0, 3)
+        st.zero_()
+        for t in (out, lse):
+            assert torch.all(t[0] == 7) and torch.all(t[2] == 7)
+        run()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.equal(out[1], want[0]) and torch.equal(lse[1], want[1])
