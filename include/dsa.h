@@ -238,11 +238,11 @@ int dsa_sparse_mla_noalloc(const void* q, const void* kv, const int32_t* offsets
  * without faulting or hanging the GPU.
  *
  * The next n_launches attention launches in this process (from
- * dsa_sparse_mla, dsa_decode_step, dsa_sparse_mla_noalloc or dsa_paged_mla)
- * initialise their
- * query barrier with one expected arrival more than will ever come, and limit
- * every pipeline wait to wait_limit_ns (1 ms to 1 s).  The wait runs out; the
- * kernel stops its pipeline, waits (bounded) for its own copies and tensor
+ * dsa_sparse_mla, dsa_decode_step, dsa_sparse_mla_noalloc, dsa_paged_mla or
+ * dsa_paged_weights) initialise their query barrier with one expected arrival
+ * more than will ever come, and limit every pipeline wait to wait_limit_ns
+ * (1 ms to 1 s).  The wait runs out; the kernel stops its pipeline, waits
+ * (bounded) for its own copies and tensor
  * core work, releases its tensor memory and writes DSA_ERR_TIMEOUT into
  * *dev_status.  The output of such a launch is undefined; the launches after
  * it run normally.  n_launches = 0 cancels.  Returns DSA_ERR_INVALID_ARG for

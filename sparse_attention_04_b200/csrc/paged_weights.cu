@@ -74,6 +74,7 @@ struct PagedWeightsParams {
   float* acc_out;
   int64_t ld_slots;
   int32_t* status;
+  int debug_stall;
   uint64_t wait_limit_ns;
 };
 
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
-      for (int i = 0; i < kNumBar; ++i) mbar_init(bar(i), i >= kSEmpty && i < kSEmpty + 2 ? kEpiWarps : 1);
+      for (int i = 0; i < kNumBar; ++i)
+        mbar_init(bar(i), i == kQFull ? 1 + p.debug_stall : i >= kSEmpty && i < kSEmpty + 2 ? kEpiWarps : 1);
       fence_mbar_init();
     }
     __syncwarp();
@@ -232,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t on = elect_one();
     const int nbox = kChunk / p.box;
     const int32_t pool_rows = (int32_t)(p.pool.n_pages * p.pool.page_size);
-    uint32_t tiles = 0, fills = 0;  // query tiles and ring places filled so far
+    uint32_t tiles = 0, fills = 0;  // query tiles asked for and ring places filled so far
     bool ok = true;
     auto place_free = [&]() {
       return warp_wait(bar(kKEmpty + fills % kPlaces), ((fills / kPlaces) & 1) ^ 1, abort, p.wait_limit_ns);
     };
     while (ok && wk.next(p)) {
-      for (int qt = 0; ok && qt < n_tiles; ++qt, ++tiles) {
+      for (int qt = 0; ok && qt < n_tiles; ++qt) {
         const int yq = wk.seq * th + qt * kRows;
         // blocks 0-7 of the query tile go through the ring, on their way to TMEM
 #pragma unroll 1
@@ -261,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(sbase + kQ8Off, &tm_q, (kKB - 1) * 64, yq, bar(kQFull));
         }
         __syncwarp();
+        ++tiles;
         for (int i = wk.lo; ok && i < wk.hi; ++i) {
           const int64_t s = (int64_t)i * kChunk + lane * p.box;
           int32_t y = pool_rows;  // outside the pool: zeros
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int never = 0;
       for (uint32_t k = fills > (uint32_t)kPlaces ? fills - kPlaces : 0; k < fills; ++k)
         mbar_wait(bar(kKFull + k % kPlaces), (k / kPlaces) & 1, &never, 10000000ull);
-      mbar_wait(bar(kQFull), tiles & 1, &never, 10000000ull);
+      if (tiles > 0) mbar_wait(bar(kQFull), (tiles - 1) & 1, &never, 10000000ull);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t on = elect_one();
@@ -488,7 +491,10 @@ extern "C" int dsa_paged_weights(const void* q, const void* kv_pages, const int3
   p.acc_out = acc_out;
   p.ld_slots = ld_slots;
   p.status = dev_status;
-  p.wait_limit_ns = kWaitLimitNs;
+  MlaParams debug;
+  take_attention_debug(debug);
+  p.debug_stall = debug.debug_stall;
+  p.wait_limit_ns = debug.wait_limit_ns;
   CUtensorMap tq, tk;
   if (!make_tmap_2d(&tq, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kDQK, (uint64_t)B * T * H, kDQK * 2, 64, kRows,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -271,3 +271,25 @@ def test_two_overlapping_calls_that_share_a_workspace_stay_inside_their_arrays(c
         run()
         torch.cuda.synchronize()
         assert int(st.item()) == 0 and torch.equal(out[1], want[0]) and torch.equal(lse[1], want[1])
+
+
+@pytest.mark.parametrize("H,T", [(128, 1), (100, 3)])
+def test_weights_wait_runs_out_then_the_next_call_is_right(cuda_device, H, T):
+    """The test hook on the accumulated weights: a launch that gives up reports it."""
+    from test_paged_gpu import Cache, _attend as attend, _check_weights, _q
+    L = _lib()
+    c = Cache(cuda_device, [9000, 40, 0, 700], 64, seed=40)
+    q = _q(c, 4, T, H)
+    _, lse, st = attend(c, q)
+    assert st == 0
+    acc = torch.rand(4, 9000, generator=c.g, device=c.dev)
+    L.debug_stall_attention(2, 2_000_000)
+    try:
+        for _ in range(2):
+            out, status = torch.zeros_like(acc), torch.zeros(1, dtype=torch.int32, device=c.dev)
+            L.paged_weights(q, c.kv, c.table, c.lens, lse, SCALE, acc, acc_out=out, status=status)
+            assert int(status.item()) == 5
+    finally:
+        L.debug_stall_attention(0, 0)
+    _, st = _check_weights(c, q, lse, acc, 0.5)
+    assert st == 0
