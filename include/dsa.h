@@ -248,9 +248,9 @@ int dsa_sparse_mla_noalloc(const void* q, const void* kv, const int32_t* offsets
  * it run normally.  n_launches = 0 cancels.  Returns DSA_ERR_INVALID_ARG for
  * a negative count or a limit outside the range.  Launches captured in a
  * CUDA graph keep the setting they were captured with.
- * With DSA_STALL_AT_PRODUCT added to n_launches, a dsa_paged_mla launch of more
- * than 32 rows a tile stalls later: scores run, messages between the SMs are on
- * their way, and the first product with the values is never issued.
+ * With DSA_STALL_AT_PRODUCT added to n_launches, a dsa_paged_mla launch stalls
+ * later: scores run, messages between SMs are on their way, and the first
+ * product with the values is never issued.
  */
 #define DSA_STALL_AT_PRODUCT (1 << 30)
 int dsa_debug_stall_attention(int n_launches, uint64_t wait_limit_ns);

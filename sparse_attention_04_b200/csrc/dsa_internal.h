@@ -125,8 +125,8 @@ struct MlaParams {
   int dense;         // no index list: row r attends to its whole causal prefix
   // Test hook (dsa_debug_stall_attention): the query barrier expects this many
   // arrivals more than will ever come, so its wait runs out and the kernel
-  // takes its timeout path.  (2 in the paged attention's CTA pair: the first
-  // message's barrier instead.)  0 in normal use.
+  // takes its timeout path.  (2 in the paged attention: the barrier before the
+  // first product with the values instead.)  0 in normal use.
   int debug_stall;
   uint64_t wait_limit_ns;  // limit of every pipeline wait (kWaitLimitNs in normal use)
 };

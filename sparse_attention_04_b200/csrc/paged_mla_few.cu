@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_q);
-      mbar_init(bar(kQFull), 1 + p.debug_stall);
+      mbar_init(bar(kQFull), 1 + (p.debug_stall & 1));
       mbar_init(bar(kQFree), 1);
       for (int i = 0; i < L::kRing; ++i) {
         mbar_init(bar(kFull + i), 1);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(kSFull + i), 1);
         mbar_init(bar(kSEmpty + i), 4);
-        mbar_init(bar(kPReady + i), kConsumers / 32);
+        mbar_init(bar(kPReady + i), kConsumers / 32 + (i == 0 ? p.debug_stall >> 1 : 0));
         mbar_init(bar(kPvDone + i), 1);
         mbar_init(bar(kDrain + i), 1);
       }
@@ -350,8 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* const alphas = reinterpret_cast<float*>(smem + L::kAlphaOff);
     int32_t* const seen = reinterpret_cast<int32_t*>(smem + L::kSeenOff);
     uint32_t g = 0;
-    bool ok = true;
-    while (ok && wk.next(p)) {
+    // A warp whose wait ran out says so at the next barrier, and all eight leave
+    // there: one that left by itself would be waited for without end.
+    bool ok = true, leave = false;
+    while (!leave && wk.next(p)) {
       if (threadIdx.x < R) seen[threadIdx.x] = wk.len - max(0, wk.nt - 1 - (int)threadIdx.x / p.H);
       const int min_len = wk.len - (wk.nt - 1);
       float m_run[C], l_run[C];
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       named_barrier_sync(1, kConsumers);
       for (int i = wk.lo; i < wk.hi; ++i, ++g) {
-        ok = wait(kMaskFull + (g & 3), (g >> 2) & 1) && wait(kSFull + (g & 1), (g >> 1) & 1);
+        ok = ok && wait(kMaskFull + (g & 3), (g >> 2) & 1) && wait(kSFull + (g & 1), (g >> 1) & 1);
         const int64_t s0 = (int64_t)i * kChunk;
         uint32_t sv[C];
         bool rise = false;
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // with a maximum that rose casts one; all eight warps go the same way.
         const uint32_t votes = named_barrier_count(1, kConsumers, !ok || (rise && lane == 0));
         if (votes >= 32) {
-          ok = false;
+          leave = true;
           break;
         }
         if (scores) {
@@ -496,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         warp_arrive(bar(kPReady + (g & 1)));
       }
-      if (!ok) break;
+      if (leave) break;
       const bool any = wk.lo < wk.hi;
-      if (any) ok = wait(kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+      if (any && ok) ok = wait(kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
       // the lanes' sums; the buffers of the maxima and factors are free: all
       // warps have read them (they arrived at kPReady since)
       float* const sums = maxima + (g & 1) * 2 * R;
@@ -512,10 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (slot == 0) alphas[cb + c] = m_run[c];
         }
       }
-      if (named_barrier_count(1, kConsumers, !ok) != 0) {
-        ok = false;
-        break;
-      }
+      if (named_barrier_count(1, kConsumers, !ok) != 0) break;
       tc_fence_after();
       const bool whole = wk.hi - wk.lo == wk.chunks;
       const int64_t part = 2 * (int64_t)blockIdx.x + (wk.lo > 0 ? 0 : 1);

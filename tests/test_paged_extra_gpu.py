@@ -293,3 +293,31 @@ def test_weights_wait_runs_out_then_the_next_call_is_right(cuda_device, H, T):
         L.debug_stall_attention(0, 0)
     _, st = _check_weights(c, q, lse, acc, 0.5)
     assert st == 0
+
+
+@pytest.mark.parametrize("lens,T", [([100], 1), ([148 * 64], 1), ([2 * 148 * 64], 2), ([3 * 148 * 64], 1), ([60000, 7000, 0], 2),
+                                    ([3000, 40, 0, 700] * 40, 1)])
+def test_few_rows_give_up_together_in_mid_stream(cuda_device, lens, T):
+    """The same for tiles of few rows, whose eight consumer warps meet in every
+    chunk: scores that rise from chunk to chunk make them wait for the product
+    that never comes in each of the places where they can."""
+    L, B, H = _lib(), len(lens), 16
+    g = torch.Generator(device=cuda_device).manual_seed(6)
+    per = max(-(-n // 64) for n in lens)
+    kv = torch.randn(per, 64, D, generator=g, device=cuda_device)
+    kv[..., 0] = torch.arange(per, device=cuda_device)[:, None]
+    kv = kv.to(torch.bfloat16)
+    table = torch.arange(per, dtype=torch.int32, device=cuda_device).expand(B, per).contiguous()
+    q = torch.randn(B, T, H, D, generator=g, device=cuda_device)
+    q[..., 0] = 160.0  # 11 and more per chunk after scaling: the maximum rises by more than 2^8
+    q = q.to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    want = _attend(q, kv, table, n)
+    assert want[2] == 0
+    L.debug_stall_attention(20, 1_000_000, at_product=True)
+    try:
+        assert [_attend(q, kv, table, n)[2] for _ in range(20)] == [5] * 20
+    finally:
+        L.debug_stall_attention(0, 0)
+    out, lse, st = _attend(q, kv, table, n)
+    assert st == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
