@@ -57,7 +57,7 @@ typedef enum {
   DSA_OK = 0,
   DSA_ERR_INVALID_ARG = 1, /* bad pointer, size, alignment or enum       */
   DSA_ERR_UNSUPPORTED = 2, /* valid but not implemented (e.g. H > 128)  */
-  DSA_ERR_WORKSPACE = 3,   /* workspace NULL or smaller than required   */
+  DSA_ERR_WORKSPACE = 3,   /* workspace NULL or smaller than required; device: shared by two calls at once */
   DSA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed         */
   DSA_ERR_TIMEOUT = 5,     /* device: a pipeline wait ran out of time   */
   DSA_ERR_BAD_INDEX = 6,   /* device: an index outside [0, end_pos)     */
